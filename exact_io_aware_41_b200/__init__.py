@@ -27,6 +27,8 @@ DECODE_STATIC_SCRATCH_BYTES = 48 << 20  # ATTN_DECODE_STATIC_SCRATCH_BYTES
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
+_Z = ctypes.c_size_t
 SIGNATURES = {
     "attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "attn_decode_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
@@ -44,6 +46,13 @@ SIGNATURES = {
     "attn_fwd_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "attn_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "attn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, ctypes.c_size_t, _P]),
+    "attn_fwd_varlen_workspace_bytes": (_Z, [_I, _I]),
+    "attn_fwd_varlen": (_I, [_P] * 7 + [_I] * 6 + [_L, _L, _L, _F, _I, _P, _Z, _P]),
+    "attn_bwd_varlen_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "attn_bwd_varlen": (_I, [_P] * 11 + [_I] * 6 + [_L, _L, _L, _F, _I, _P, _Z, _P]),
+    "attn_decode_paged_workspace_bytes": (_Z, [_I, _I, _I, _I]),
+    "attn_decode_paged": (_I, [_P] * 5 + [_I, _I, _I, _P, _P, _I, _I, _I, _I, _L, _F, _P, _Z, _P]),
+    "attn_cache_append": (_I, [_P] * 7 + [_I] * 7 + [_L, _L, _P]),
 }
 
 
@@ -324,3 +333,237 @@ def attn_bwd(q, k, v, o, lse, dout, scale: float | None = None, causal: bool = F
                                  workspace.numel() * workspace.element_size(), _stream(stream))
     _check("attn_bwd", code)
     return dq, dk, dv
+
+
+# ---- packed sequences and the paged cache --------------------------------------------------------------
+# These run on the device of their first tensor, whatever the current device is, and allocate what the
+# caller does not pass on the stream they run on, so that torch's allocator never hands that memory to
+# other work before the call is done with it.
+
+def _on(t, stream):
+    """Context in which allocations and the launch belong to t's device and the given stream."""
+    import contextlib
+    import torch
+
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _token_rows(name, t, ndim, device=None):
+    """Checks a bf16 [.., tokens, heads, d] operand whose tokens may be a stride apart; returns that stride."""
+    import torch
+
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != ndim:
+        raise ValueError(f"{name} must be a {ndim}-d bf16 CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return sn if n > 1 else h * d
+
+
+def _dense(name, t, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _int32(name, t, ndim, device):
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or t.dim() != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ndim}-d int32 tensor on {device}")
+
+
+def _workspace(workspace, need, device):
+    import torch
+
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _varlen_shapes(q, k, v, cu_q, cu_k):
+    dev = q.device
+    qs = _token_rows("q", q, 3)
+    ks = _token_rows("k", k, 3, dev)
+    vs = _token_rows("v", v, 3, dev)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
+    _int32("cu_seqlens_q", cu_q, 1, dev)
+    if cu_k is not cu_q:
+        _int32("cu_seqlens_k", cu_k, 1, dev)
+    if cu_q.shape != cu_k.shape or cu_q.numel() < 2:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have one entry more than there are sequences")
+    return dev, qs, ks, vs
+
+
+def attn_fwd_varlen_workspace_bytes(S: int, Tq: int) -> int:
+    return int(lib_handle().attn_fwd_varlen_workspace_bytes(S, Tq))
+
+
+def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale: float | None = None, causal: bool = False,
+                    workspace=None, out=None, lse=None, stream=None):
+    """Prefill over packed sequences. q [Tq, Hq, d], k and v [Tk, Hkv, d] (bf16, CUDA; tokens may be a stride
+    apart, a token's heads are dense); cu_seqlens_* int32 [S + 1] (CUDA): sequence s owns rows cu[s] .. cu[s + 1)
+    (cu_seqlens_k None: the same as cu_seqlens_q). causal: query i of a sequence sees key j iff
+    j <= i + Nkv - Nq. Rows that no sequence owns are left as they were (undefined in fresh outputs).
+
+    Returns (O [Tq, Hq, d] bf16, LSE [Hq, Tq] fp32).
+    """
+    import torch
+
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    dev, qs, ks, vs = _varlen_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    Tq, Hq, d = q.shape
+    Tk, Hkv, _ = k.shape
+    S = cu_seqlens_q.numel() - 1
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = lib_handle()
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty((Tq, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense("out", out, torch.bfloat16, (Tq, Hq, d), dev)
+        if lse is None:
+            lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
+        else:
+            _dense("lse", lse, torch.float32, (Hq, Tq), dev)
+        workspace = _workspace(workspace, lib.attn_fwd_varlen_workspace_bytes(S, Tq), dev)
+        code = lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
+                                   cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs,
+                                   ks, vs, float(scale), int(bool(causal)), workspace.data_ptr(), workspace.nbytes,
+                                   _stream(stream))
+    _check("attn_fwd_varlen", code)
+    return out, lse
+
+
+def attn_bwd_varlen_workspace_bytes(S: int, Tq: int, Tk: int, Hq: int, d: int) -> int:
+    return int(lib_handle().attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d))
+
+
+def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k=None, scale: float | None = None,
+                    causal: bool = False, workspace=None, dq=None, dk=None, dv=None, stream=None):
+    """Backward pass of attn_fwd_varlen (d = 128). q, k, v and the offsets as given there, o and lse as it
+    returned them, dout [Tq, Hq, d] like o. Returns (dQ, dK, dV), dense, in the shapes of q, k, v."""
+    import torch
+
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    dev, qs, ks, vs = _varlen_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    Tq, Hq, d = q.shape
+    Tk, Hkv, _ = k.shape
+    S = cu_seqlens_q.numel() - 1
+    bf16 = torch.bfloat16
+    _dense("o", o, bf16, (Tq, Hq, d), dev)
+    _dense("dout", dout, bf16, (Tq, Hq, d), dev)
+    _dense("lse", lse, torch.float32, (Hq, Tq), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = lib_handle()
+    with _on(q, stream):
+        grads = []
+        for name, g, shape in (("dq", dq, q.shape), ("dk", dk, k.shape), ("dv", dv, v.shape)):
+            if g is None:
+                g = torch.empty(shape, dtype=bf16, device=dev)
+            else:
+                _dense(name, g, bf16, shape, dev)
+            grads.append(g)
+        dq, dk, dv = grads
+        workspace = _workspace(workspace, lib.attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d), dev)
+        code = lib.attn_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                   dout.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), dq.data_ptr(),
+                                   dk.data_ptr(), dv.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks, vs, float(scale),
+                                   int(bool(causal)), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check("attn_bwd_varlen", code)
+    return dq, dk, dv
+
+
+def _pool_shape(k_pages, v_pages, page_table, kv_lens, dev):
+    import torch
+
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous [n_pages, page_size, Hkv, d] bf16 tensor on {dev}")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    _int32("page_table", page_table, 2, dev)
+    _int32("kv_lens", kv_lens, 1, dev)
+    if page_table.shape[0] != kv_lens.shape[0]:
+        raise ValueError("page_table must be [B, max_pages] and kv_lens [B]")
+    return k_pages.shape
+
+
+def attn_decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib_handle().attn_decode_paged_workspace_bytes(B, Hq, Hkv, d))
+
+
+def attn_decode_paged(q, k_pages, v_pages, page_table, kv_lens, scale: float | None = None, workspace=None, out=None,
+                      lse=None, stream=None):
+    """Attention of one query token per sequence over a paged KV cache. q [B, Hq, d] (sequences may be a stride
+    apart); k_pages, v_pages [n_pages, page_size, Hkv, d]; page_table int32 [B, max_pages]; kv_lens int32 [B]:
+    token t of sequence b is row t % page_size of page page_table[b, t // page_size].
+
+    Returns (O [B, Hq, d] bf16, LSE [B, Hq] fp32).
+    """
+    import torch
+
+    dev = q.device
+    qs = _token_rows("q", q, 3)
+    n_pages, page_size, Hkv, _ = _pool_shape(k_pages, v_pages, page_table, kv_lens, dev)
+    B, Hq, d = q.shape
+    if k_pages.shape[3] != d or kv_lens.shape[0] != B:
+        raise ValueError("k_pages must have q's d, kv_lens and page_table q's B")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = lib_handle()
+    with _on(q, stream):
+        if out is None:
+            out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense("out", out, torch.bfloat16, (B, Hq, d), dev)
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        else:
+            _dense("lse", lse, torch.float32, (B, Hq), dev)
+        workspace = _workspace(workspace, lib.attn_decode_paged_workspace_bytes(B, Hq, Hkv, d), dev)
+        code = lib.attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                     kv_lens.data_ptr(), n_pages, page_size, page_table.shape[1], out.data_ptr(),
+                                     lse.data_ptr(), B, Hq, Hkv, d, qs, float(scale), workspace.data_ptr(),
+                                     workspace.nbytes, _stream(stream))
+    _check("attn_decode_paged", code)
+    return out, lse
+
+
+def attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, stream=None) -> None:
+    """Writes new rows of K and V [T, Hkv, d] into the pages of their sequences, in place. cu_seqlens int32
+    [B + 1]: sequence b's new rows are cu[b] .. cu[b + 1) (None: one row per sequence, T = B); kv_lens int32 [B]
+    are the lengths with the new rows, so the last of them becomes token kv_lens[b] - 1."""
+    dev = k_pages.device
+    n_pages, page_size, Hkv, d = _pool_shape(k_pages, v_pages, page_table, kv_lens, dev)
+    ks = _token_rows("k_new", k_new, 3, dev)
+    vs = _token_rows("v_new", v_new, 3, dev)
+    T, B = k_new.shape[0], kv_lens.shape[0]
+    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (Hkv, d):
+        raise ValueError("k_new and v_new must be [T, Hkv, d] with the pool's Hkv and d")
+    if cu_seqlens is not None:
+        _int32("cu_seqlens", cu_seqlens, 1, dev)
+        if cu_seqlens.shape[0] != B + 1:
+            raise ValueError("cu_seqlens must be [B + 1]")
+    with _on(k_pages, stream):
+        code = lib_handle().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(),
+                                              None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                                              page_table.data_ptr(), kv_lens.data_ptr(), k_pages.data_ptr(),
+                                              v_pages.data_ptr(), B, T, n_pages, page_size, page_table.shape[1], Hkv, d,
+                                              ks, vs, _stream(stream))
+    _check("attn_cache_append", code)

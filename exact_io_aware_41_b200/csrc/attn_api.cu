@@ -365,7 +365,7 @@ attn_status_t attn_get_last_error(void) {
   if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) return ATTN_ERR_CUDA;
   if (word & kErrTimeoutBit) return ATTN_ERR_TIMEOUT;
   if (word & kErrSmemAlignBit) return ATTN_ERR_CUDA;
-  if (word & kErrBadLengthBit) return ATTN_ERR_INVALID_ARG;
+  if (word & (kErrBadLengthBit | kErrBadPageBit)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
@@ -387,6 +387,9 @@ const char* attn_kernel_name(int which) {
     case 1: return "attn::decode_split_tc_kernel<D,G> (d <= 128), attn::decode_split_kernel<D,G> (d = 256)";
     case 2: return "attn::decode_combine_kernel<D>";
     case 3: return "attn::attn_bwd_pre_kernel, attn::attn_bwd_kernel, attn::attn_bwd_post_kernel";
+    case 4: return "attn::varlen_fwd_simple_kernel<D>";
+    case 5: return "attn::decode_paged_simple_kernel<D>";
+    case 6: return "attn::cache_append_kernel";
   }
   return nullptr;
 }

@@ -11,8 +11,9 @@ namespace attn {
 
 // Bits of the device error word (g_error_word).
 enum : unsigned int {
-  kErrBadLengthBit = 2u,  // a decode length outside [0, Nkv_cap] was clamped
+  kErrBadLengthBit = 2u,  // a decode length or a packed-sequence offset out of range
   kErrSmemAlignBit = 4u,  // a kernel found its dynamic shared memory off its required alignment
+  kErrBadPageBit = 8u,    // a page number outside the pool was clamped (reads) or skipped (writes)
 };
 
 // Wall-time limit of every pipeline wait inside a kernel. Far above any legitimate wait (a whole
@@ -37,6 +38,10 @@ struct FwdArgs {
 };
 
 bool is_aligned16(const void* p);
+// Token stride (in elements) of a [tokens, heads, d] operand that the packed and paged entry points take.
+bool token_stride_ok(long long stride, int heads, int d);
+// Most sequences of one packed call.
+constexpr int kVarMaxSeqs = 1000000;
 
 // Devices the per-device host tables cover (device ordinals 0 .. kMaxDevices-1).
 constexpr int kMaxDevices = 128;

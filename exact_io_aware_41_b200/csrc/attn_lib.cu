@@ -7,3 +7,5 @@
 #include "attn_decode_static.cu"
 #include "attn_fp8.cu"
 #include "attn_bwd.cu"
+#include "attn_varlen.cu"
+#include "attn_paged.cu"

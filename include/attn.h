@@ -207,9 +207,95 @@ attn_status_t attn_decode_combine(const float* part_o, const float* part_lse, in
                                   void* o, float* lse, cudaStream_t stream);
 
 /*
+ * Packed sequences of different lengths: prefill forward over S sequences laid end to end.
+ *
+ *   q    [Tq, Hq, d] bf16, k and v [Tk, Hkv, d] bf16, read only; consecutive tokens are q_stride,
+ *        k_stride, v_stride elements apart (a token's heads are dense, so a slice of a fused
+ *        projection can be passed as it is), each at least heads * d, a multiple of 8 and below 2^31
+ *   cu_q, cu_k  int32 [S + 1] in device memory: sequence s has query rows cu_q[s] .. cu_q[s + 1) and keys
+ *        cu_k[s] .. cu_k[s + 1); 0 <= cu[s] <= cu[s + 1] <= Tq (Tk). Sequences may be empty. The same
+ *        array may be given twice.
+ *   o    [Tq, Hq, d] bf16, dense, written;  lse [Hq, Tq] fp32, written
+ *   causal = 1: query i of a sequence sees its key j iff j <= i + Nkv - Nq, with the sequence's own
+ *        lengths. A query that sees no key (an empty key range included) gets O = 0 and LSE = -inf.
+ *   workspace   at least attn_fwd_varlen_workspace_bytes(S, Tq) bytes, 256-byte aligned, no
+ *        initialisation needed. Calls that may overlap on the GPU need workspaces of their own.
+ *   S, Tq, Tk, Hq, Hkv >= 1, S <= 1000000, d in {32, 64, 128, 256}; scale as attn_fwd.
+ * Rows of q that no sequence owns (before cu_q[0], from cu_q[S] on) are not read by any sequence's result
+ * and their rows of o and lse are left as they were; what rows of other sequences hold, NaN and infinities
+ * included, never reaches a sequence's result. Offsets that break the order above set the device error
+ * word (ATTN_ERR_INVALID_ARG from attn_get_last_error) and nothing at all is written.
+ */
+size_t attn_fwd_varlen_workspace_bytes(int S, int Tq);
+attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const int32_t* cu_q, const int32_t* cu_k,
+                              void* o, float* lse, int S, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride,
+                              long long k_stride, long long v_stride, float scale, int causal, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Backward pass of attn_fwd_varlen: attn_bwd's gradients, sequence by sequence.
+ *   q, k, v, cu_q, cu_k, strides, scale, causal as given to attn_fwd_varlen; o, dout [Tq, Hq, d] bf16, dense;
+ *   lse [Hq, Tq] fp32 (from attn_fwd_varlen), all read only
+ *   dq [Tq, Hq, d], dk, dv [Tk, Hkv, d] bf16, dense, written: every row that a sequence owns (0 where
+ *        nothing depends on it); the other rows are left as they were
+ *   workspace   at least attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d) bytes, 256-byte aligned, no
+ *        initialisation needed
+ *   d = 128 (ATTN_ERR_UNSUPPORTED otherwise); everything else as attn_fwd_varlen.
+ */
+size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d);
+attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                              const void* dout, const int32_t* cu_q, const int32_t* cu_k, void* dq, void* dk, void* dv,
+                              int S, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                              long long v_stride, float scale, int causal, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/*
+ * Paged KV cache. A pool holds n_pages pages of page_size tokens, k_pages and v_pages
+ * [n_pages, page_size, Hkv, d] bf16, dense; page_table int32 [B, max_pages] (device) names the pages of
+ * each sequence: token t of sequence b is row t % page_size of page page_table[b][t / page_size]. Entries
+ * past a sequence's last page are not read. Pages may be shared between sequences. page_size is a multiple
+ * of 16, at most 65536 (ATTN_ERR_UNSUPPORTED otherwise).
+ *
+ * attn_decode_paged: attention of one query token per sequence over its pages, split over the cache's
+ * length and joined ("FlashAttention evolution", section 6).
+ *   q    [B, Hq, d] bf16, consecutive sequences q_stride elements apart (as in attn_fwd_varlen)
+ *   kv_lens  int32 [B] (device), each in [0, max_pages * page_size]; other values are clamped and
+ *        flagged in the device error word, and so are page numbers outside [0, n_pages)
+ *   o    [B, Hq, d] bf16, dense, written;  lse [B, Hq] fp32, written (O = 0 and LSE = -inf where kv_lens[b] = 0)
+ *   d in {32, 64, 128, 256}; Hq / Hkv from 1 to 16 (ATTN_ERR_UNSUPPORTED otherwise)
+ *   workspace   at least attn_decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes, 16-byte aligned, no
+ *        initialisation needed; its size does not depend on the cache's length
+ * Rows of a page behind the end of its sequence may hold anything.
+ */
+size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
+attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                                const int32_t* kv_lens, int n_pages, int page_size, int max_pages, void* o, float* lse,
+                                int B, int Hq, int Hkv, int d, long long q_stride, float scale, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_cache_append: writes T new rows of K and V into the pages of their sequences.
+ *   k_new, v_new  [T, Hkv, d] bf16, token strides as in attn_fwd_varlen, read only
+ *   cu   int32 [B + 1] (device): sequence b's new rows are cu[b] .. cu[b + 1), 0 <= cu[b] <= cu[b + 1] <= T; or
+ *        NULL: one row per sequence, T = B (ATTN_ERR_INVALID_ARG otherwise)
+ *   kv_lens  int32 [B] (device): the sequences' lengths WITH the new rows, so that the i-th of the n new rows of
+ *        sequence b becomes its token kv_lens[b] - n + i; the array is not changed
+ *   page_table, k_pages, v_pages as above; the pages the new tokens fall into have to be in the table
+ * A row whose position is outside [0, max_pages * page_size) or whose page is outside [0, n_pages) is not
+ * written and flagged in the device error word; rows that no sequence owns are ignored. Two rows that fall on
+ * the same place (a page shared between growing sequences) race. Hkv, d >= 1, Hkv * d a multiple of 8;
+ * any page_size >= 1.
+ */
+attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int32_t* cu, const int32_t* page_table,
+                                const int32_t* kv_lens, void* k_pages, void* v_pages, int B, int T, int n_pages,
+                                int page_size, int max_pages, int Hkv, int d, long long k_stride, long long v_stride,
+                                cudaStream_t stream);
+
+/*
  * Reads and clears the device error word (synchronises the calling thread with the device).
  * ATTN_OK if no kernel recorded a fault since the last call, ATTN_ERR_TIMEOUT if a bounded
- * pipeline wait gave up, ATTN_ERR_INVALID_ARG if a decode length was out of range, ATTN_ERR_CUDA
+ * pipeline wait gave up, ATTN_ERR_INVALID_ARG if a decode length, a page number or the offsets of packed
+ * sequences were out of range, ATTN_ERR_CUDA
  * if the word could not be read or a kernel found its shared memory misaligned (and did nothing).
  */
 attn_status_t attn_get_last_error(void);
@@ -219,8 +305,9 @@ const char* attn_status_string(attn_status_t status);
 
 /*
  * Name of the kernel(s) that `which` selects (0 = prefill forward, bf16 or 8-bit, 1 = decode split,
- * 2 = decode combine, 3 = backward), for recording which kernel a measurement ran (the evolution article's section 1.1
- * asks that a benchmark name its kernel). Returns NULL for an unknown index.
+ * 2 = decode combine, 3 = backward, 4 = packed prefill, 5 = paged decode, 6 = cache append), for
+ * recording which kernel a measurement ran (the evolution article's section 1.1 asks that a benchmark
+ * name its kernel). Returns NULL for an unknown index.
  */
 const char* attn_kernel_name(int which);
 
