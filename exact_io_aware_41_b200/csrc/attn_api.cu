@@ -388,7 +388,7 @@ const char* attn_kernel_name(int which) {
     case 2: return "attn::decode_combine_kernel<D>";
     case 3: return "attn::attn_bwd_pre_kernel, attn::attn_bwd_kernel, attn::attn_bwd_post_kernel";
     case 4: return "attn::varlen_fwd_simple_kernel<D>";
-    case 5: return "attn::decode_paged_simple_kernel<D>";
+    case 5: return "attn::decode_paged_kernel<D, NH>, attn::decode_paged_join_kernel<D, NH>";
     case 6: return "attn::cache_append_kernel";
   }
   return nullptr;

@@ -1,5 +1,5 @@
 // Paged KV cache: single-token attention over it (attn_decode_paged) and the writes into it
-// (attn_cache_append). Plain decode kernel: one warp per query head row, tokens one after the other.
+// (attn_cache_append).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -27,46 +27,579 @@ __device__ __forceinline__ int page_in_pool(int p, int n_pages) {
   return p;
 }
 
+// ---------------------------------------------------------------------------------------------
+// Split kernel. The work of a call is the list of 64-token tiles of every (sequence b, kv head g), in that
+// order; CTA i of N takes the contiguous share [i W / N, (i + 1) W / N) of the W tiles. Every CTA so streams
+// the same number of bytes whatever the lengths are, and neither the grid nor the workspace depends on the
+// capacity of the page table. A share covers whole (b, g) pairs, whose output is written here, and at its ends
+// parts of pairs that other CTAs share: those leave (m, l, unnormalised O) in a workspace slot, at most two per
+// CTA, and the join kernel below merges them.
+//
+// A producer warp streams the tiles through a ring of shared-memory stages with TMA, one box per page (or per
+// 64 tokens of a larger page), one lane per box. Each of the NW consumer warps takes 16 tokens of every tile
+// and runs both products on warp-level tensor cores with the tokens (S^T = K Q^T) and the head dim
+// (O^T += V^T P^T) as the 16 MMA rows and the group's query heads as its 8 columns: no accumulator register
+// and no MMA is spent on padding beyond a group of 8, and d = 256 fits the register file. S^T leaves the
+// MMA with a token's two heads per lane; movmatrix transposes the bf16 P into the B operand.
+// ---------------------------------------------------------------------------------------------
+constexpr int kPagedMaxCtas = 320;   // most CTAs of a launch (two per SM; bounds the workspace)
+constexpr int kPagedMinTiles = 4;    // tiles of a share, at least (fewer CTAs for little work)
+
+template <int D, int NH>
+struct PagedCfg {
+  static constexpr int NW = 4;                  // consumer warps
+  static constexpr int TT = 16 * NW;            // tokens per tile
+  static constexpr int CE = D < 64 ? D : 64;    // elements of a stored row: one swizzle chunk
+  static constexpr int ROWB = CE * 2;
+  static constexpr int NCHUNK = D / CE;
+  static constexpr int CHUNK_BYTES = TT * ROWB;
+  static constexpr int TILE_BYTES = TT * D * 2;  // one K or V tile
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int HEADS = 8 * NH;          // query heads of a group, padded
+  static constexpr int MERGE_FLOATS = HEADS * (D + 2);  // one warp's (O, m, l)
+  static constexpr int MERGE_BYTES = (NW - 1) * MERGE_FLOATS * 4;
+  static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
+  static constexpr int SMEM_CAP = (CTAS == 1 ? 227 : 113) * 1024;
+  static constexpr int FIT = (SMEM_CAP - 1024 - MERGE_BYTES - 512) / STAGE_BYTES;
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static_assert(STAGES >= 2, "a ring of two stages at least");
+  static constexpr int THREADS = 32 * (NW + 1);
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + MERGE_BYTES + 16 * STAGES + 2 * STAGES * 8 + 128;
+  static_assert(SMEM_BYTES <= SMEM_CAP, "shared memory budget");
+};
+
+// What a stage of the ring holds, written by the producer with the tile: the consumers go by this alone.
+struct __align__(16) PagedTile {
+  int b, g;
+  int valid;  // tokens of the tile inside the sequence (the first ones), 1 .. 64
+  int flags;  // kTileFirst ..: the tile's place in its segment (a CTA's part of one (b, g) pair)
+};
+enum : int {
+  kTileFirst = 1,   // first tile of a segment
+  kTileLast = 2,    // last one
+  kTileWhole = 4,   // the segment is the whole (b, g) pair: its output is final
+  kTileStart = 8,   // the segment starts the pair (else it continues it)
+};
+
+struct PagedArgs {
+  const __nv_bfloat16* q;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  int n_pages, page_size, max_pages;
+  int box;           // tokens of a TMA box: the part of a tile that lies in one page
+  __nv_bfloat16* o;
+  float* lse;
+  int B, Hq, Hkv, G;
+  long long q_stride;
+  float scale_log2;
+  long long* head;   // workspace: W, N, then the tiles before each sequence and all of them [B + 1]
+  float* parts;      // workspace: [2 * CTA + end] slots of HEADS x D (O), HEADS (m), HEADS (l)
+  unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Programmatic dependent launch: the next kernel of the stream may start its preamble, and waits here until
+// this one's results are in memory.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Byte address of element (row, col) of a tile written by TMA: 128-byte swizzled chunks of 64 columns, or
+// plain 64-byte rows at d = 32.
 template <int D>
-__global__ void __launch_bounds__(128)
-    decode_paged_simple_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kp,
-                               const __nv_bfloat16* __restrict__ vp, const int32_t* __restrict__ table,
-                               const int32_t* __restrict__ kv_lens, int n_pages, int page_size, int max_pages,
-                               __nv_bfloat16* __restrict__ o, float* __restrict__ lse, int B, int Hq, int Hkv,
-                               long long q_stride, float scale) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5;
-  if (w >= (long long)B * Hq) return;
-  const int b = int(w / Hq), h = int(w % Hq), g = h / (Hq / Hkv);
-  const int L = paged_len(kv_lens, b, (long long)max_pages * page_size);
-  float qf[D / 32], x[D / 32], acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    qf[i] = __bfloat162float(q[b * q_stride + h * D + lane + 32 * i]);
-    acc[i] = 0.f;
+__device__ __forceinline__ uint32_t paged_at(uint32_t tile, int row, int col) {
+  constexpr int CHUNK_BYTES = PagedCfg<D, 1>::CHUNK_BYTES;
+  if constexpr (D >= 64)
+    return tile + (col >> 6) * CHUNK_BYTES + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+  else
+    return tile + row * 64 + (col << 1);
+}
+
+template <int D, int NH>
+__global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTAS)
+    decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const PagedArgs a) {
+  using C = PagedCfg<D, NH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* merge = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
+  volatile PagedTile* tile_of =
+      reinterpret_cast<volatile PagedTile*>(smem + C::STAGES * C::STAGE_BYTES + C::MERGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::MERGE_BYTES + 16 * C::STAGES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* join_full = empty + C::STAGES;  // one phase per segment: warps 1 .. NW - 1 left theirs in `merge`
+  uint64_t* join_free = join_full + 1;      // one phase per segment: warp 0 has read it
+  long long* s_base = reinterpret_cast<long long*>(join_free + 1);  // tiles before s_seq's
+  long long* s_warp = s_base + 1;                                   // [NW + 1] per-warp tile sums
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(s_warp + C::NW + 1);
+  volatile int* s_seq = abort_flag + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t T = a.timeout_ns;
+  const long long cap = (long long)a.max_pages * a.page_size;
+  auto tiles_of = [&](int b) -> int { return int((paged_len(a.kv_lens, b, cap) + (long long)C::TT - 1) / C::TT); };
+
+  pdl_launch();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], C::NW);
+    }
+    mbar_init(join_full, C::NW - 1);
+    mbar_init(join_free, 1);
+    *abort_flag = 0;
+    *s_seq = a.B;
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
   }
-  float m = -INFINITY, l = 0.f;
-  for (int t = 0; t < L; ++t) {
-    const int p = page_in_pool(table[size_t(b) * max_pages + t / page_size], n_pages);
-    const size_t row = ((size_t(p) * page_size + t % page_size) * Hkv + g) * D;
-    float s = 0.f;
+  // ---- this CTA's share: tiles before each thread's run of sequences, by a scan over the block
+  const int per = (a.B + C::THREADS - 1) / C::THREADS;
+  const int b_lo = min(a.B, int(threadIdx.x) * per), b_hi = min(a.B, b_lo + per);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b);
+  long long scan = mine;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) s = fmaf(qf[i], __bfloat162float(kp[row + lane + 32 * i]), s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= scale;
-    const float mn = fmaxf(m, s), f = expf(m - mn), pr = expf(s - mn);
-    m = mn;
-    l = l * f + pr;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) x[i] = __bfloat162float(vp[row + lane + 32 * i]);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(pr, x[i], acc[i] * f);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += x;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (lane == 31) s_warp[warp] = scan;
+  __syncthreads();
+  long long before = scan - mine, total = 0;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) o[(size_t(b) * Hq + h) * D + lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
-  if (lane == 0) lse[size_t(b) * Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  for (int w = 0; w < C::NW + 1; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  const long long W = total * a.Hkv;
+  const long long want = (W + kPagedMinTiles - 1) / kPagedMinTiles;
+  const long long N = want < gridDim.x ? want : gridDim.x;
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) {
+      a.head[0] = W;
+      a.head[1] = N;
+    }
+    long long x = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      a.head[2 + b] = x;
+      x += tiles_of(b);
+      if (b == a.B - 1) a.head[2 + a.B] = x;
+    }
+  }
+  if (blockIdx.x >= N) return;
+  const long long begin = blockIdx.x * W / N, end = (blockIdx.x + 1ll) * W / N;
+  if (before * a.Hkv <= begin && begin < (before + mine) * a.Hkv) {
+    long long x = before;
+    int b = b_lo;
+    for (; b < b_hi - 1; ++b) {
+      const int n = tiles_of(b);
+      if (begin < (x + n) * a.Hkv) break;
+      x += n;
+    }
+    *s_seq = b;
+    *s_base = x;
+  }
+  __syncthreads();
+  const int n_tiles = int(end - begin);
+
+  if (warp == C::NW) {
+    // ================================ TMA producer ================================
+    const int subs = C::TT / a.box;  // boxes of a tile; lane k < subs loads box k
+    int b = *s_seq, L = 0, nt = 0, g = 0, t = 0;  // the tile to load next: tile t of the nt of (b, g)
+    auto page_of = [&]() -> int {  // page of this lane's box of that tile, or -1 past the sequence's end
+      const long long tok = (long long)t * C::TT + lane * a.box;
+      if (lane >= subs || tok >= L) return -1;
+      return page_in_pool(__ldg(a.table + size_t(b) * a.max_pages + int(tok / a.page_size)), a.n_pages);
+    };
+    int page = -1;
+    if (b < a.B) {
+      L = paged_len(a.kv_lens, b, cap);
+      nt = tiles_of(b);
+      const long long off = begin - *s_base * a.Hkv;
+      if (nt > 0 && off >= 0 && off < (long long)nt * a.Hkv) {
+        g = int(off / nt);
+        t = int(off % nt);
+        page = page_of();
+      }
+    }
+    int t_first = t;  // first tile of the current segment
+    int i = 0;        // tiles issued
+    bool ok = true;
+    for (; i < n_tiles; ++i) {
+      if (t >= nt) {  // (only if kv_lens changed under the call)
+        if (lane == 0) *abort_flag = 1, atomicOr(&g_error_word, kErrBadLengthBit);
+        break;
+      }
+      PagedTile now;
+      now.b = b;
+      now.g = g;
+      now.valid = int(min((long long)C::TT, L - (long long)t * C::TT));
+      now.flags = (t == t_first ? kTileFirst : 0) | (t + 1 == nt || i + 1 == n_tiles ? kTileLast : 0) |
+                  (t_first == 0 ? kTileStart : 0) | (t_first == 0 && t + 1 == nt ? kTileWhole : 0);
+      const int row = int(((long long)t * C::TT + lane * a.box) % a.page_size), cur = page;
+      // the next tile and its pages, while the stage becomes free
+      if (i + 1 < n_tiles) {
+        if (++t == nt) {
+          t = t_first = 0;
+          if (++g == a.Hkv) {
+            g = 0;
+            for (++b; b < a.B; ++b)
+              if ((nt = tiles_of(b)) > 0) break;
+            L = b < a.B ? paged_len(a.kv_lens, b, cap) : 0;
+            if (b >= a.B) nt = 0;
+          }
+        }
+        page = t < nt ? page_of() : -1;
+      }
+      const int st = i % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], uint32_t(((i / C::STAGES) & 1) ^ 1), abort_flag, T));
+      if (!ok) break;
+      const int boxes = __popc(__ballot_sync(0xffffffffu, cur >= 0));
+      if (lane == 0) {
+        tile_of[st].b = now.b;
+        tile_of[st].g = now.g;
+        tile_of[st].valid = now.valid;
+        tile_of[st].flags = now.flags;
+        mbar_arrive_expect_tx(&full[st], uint32_t(boxes * a.box * D * 2 * 2));
+      }
+      __syncwarp();
+      if (cur >= 0) {
+        uint8_t* kt = smem + st * C::STAGE_BYTES + lane * a.box * C::ROWB;
+#pragma unroll
+        for (int c = 0; c < C::NCHUNK; ++c) {
+          tma_load_4d(kt + c * C::CHUNK_BYTES, &tmK, &full[st], c * C::CE, now.g, row, cur);
+          tma_load_4d(kt + C::TILE_BYTES + c * C::CHUNK_BYTES, &tmV, &full[st], c * C::CE, now.g, row, cur);
+        }
+      }
+    }
+    if (i < n_tiles) ok = false;
+    if (!ok && lane == 0) {
+      // gave up: let the copies in flight land before the CTA exits
+      for (int st = 0; st < C::STAGES; ++st) {
+        const int fills = (i - st + C::STAGES - 1) / C::STAGES;
+        if (fills > 0) mbar_wait(&full[st], (fills - 1) & 1, nullptr, 100000000ull);
+      }
+    }
+    return;
+  }
+
+  // ================================ consumer warps ================================
+  const int gid = lane >> 2, tid = lane & 3;    // mma fragment coordinates
+  const int mi = lane >> 3, rr = lane & 7;      // ldmatrix: which 8x8 matrix this lane addresses, and its row
+  // B fragments of Q^T (columns = query heads, zero past G), one pair per 16-wide k-step
+  uint32_t qb[NH][D / 16][2];
+  // O^T rows 16 db + gid, 16 db + gid + 8, heads 8 h + 2 tid, + 1
+  float o[NH][D / 16][4];
+  float m[NH][2], l[NH][2];  // reference max (log2 units) and this lane's sum, per head
+  int seg = 0;               // segments finished (phases of join_full and join_free)
+  auto wait_warp = [&](uint64_t* bar, uint32_t ph) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag, T));
+  };
+  for (int i = 0; i < n_tiles; ++i) {
+    const int st = i % C::STAGES;
+    if (!wait_warp(&full[st], uint32_t((i / C::STAGES) & 1))) return;
+    const int b = tile_of[st].b, g = tile_of[st].g, flags = tile_of[st].flags;
+    const int valid = tile_of[st].valid - 16 * warp;  // of this warp's 16 tokens
+    if (flags & kTileFirst) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const bool real = gid + 8 * h < a.G;
+        const __nv_bfloat16* qr = a.q + b * a.q_stride + (g * a.G + (real ? gid + 8 * h : 0)) * D + 2 * tid;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qb[h][kk][0] = real ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
+          qb[h][kk][1] = real ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
+        }
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db) o[h][db][0] = o[h][db][1] = o[h][db][2] = o[h][db][3] = 0.f;
+        m[h][0] = m[h][1] = -INFINITY;
+        l[h][0] = l[h][1] = 0.f;
+      }
+    }
+    {
+      const uint32_t kt = smem_u32(smem + st * C::STAGE_BYTES);
+      const uint32_t vt = kt + C::TILE_BYTES;
+      if (valid > 0) {
+        // ---- S^T = K Q^T over 16 tokens; two chains of accumulators
+        float s[NH][2][4];
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) s[h][k][0] = s[h][k][1] = s[h][k][2] = s[h][k][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4(paged_at<D>(kt, 16 * warp + 8 * (mi & 1) + rr, kk * 16 + 8 * (mi >> 1)), a0, a1, a2, a3);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) mma_bf16_16816(s[h][kk & 1], a0, a1, a2, a3, qb[h][kk][0], qb[h][kk][1]);
+        }
+        uint32_t p[NH][2];  // P^T: B fragments of the second product
+        bool need = false;
+        float x[NH][4];  // tokens gid (0, 1) and gid + 8 (2, 3); heads 2 tid (0, 2) and 2 tid + 1 (1, 3)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[h][k] = (s[h][0][k] + s[h][1][k]) * a.scale_log2;
+            if (gid + 8 * (k >> 1) >= valid) x[h][k] = -INFINITY;
+            need |= x[h][k] - m[h][k & 1] > kDecodeTau;
+          }
+        }
+        // a score above a reference max by more than tau (the first tile: any): raise the references to the
+        // 16 tokens' max and rescale
+        if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float mx = fmaxf(x[h][k], x[h][k + 2]);
+#pragma unroll
+              for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+              if (mx - m[h][k] > kDecodeTau) {
+                const float alpha = ex2(m[h][k] - mx);
+                l[h][k] *= alpha;
+#pragma unroll
+                for (int db = 0; db < D / 16; ++db) {
+                  o[h][db][k] *= alpha;
+                  o[h][db][k + 2] *= alpha;
+                }
+                m[h][k] = mx;
+              }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          float e[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e[k] = x[h][k] == -INFINITY ? 0.f : ex2(x[h][k] - m[h][k & 1]);
+            l[h][k & 1] += e[k];
+          }
+          // rounded to bf16 for the tensor cores; the sums keep the unrounded values
+          p[h][0] = movmatrix_t(pack_bf16x2(e[0], e[1]));
+          p[h][1] = movmatrix_t(pack_bf16x2(e[2], e[3]));
+        }
+        // rows past the sequence's end may hold anything (0 * NaN would poison O): zero them
+        if (valid < 16) {
+          constexpr int UPR = C::ROWB / 16;
+          for (int idx = lane; idx < (16 - valid) * (D / 8); idx += 32) {
+            const int r = valid + idx / (D / 8), unit = idx % (D / 8);
+            const uint32_t at = vt + (unit / UPR) * C::CHUNK_BYTES + (16 * warp + r) * C::ROWB + ((unit % UPR) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+          }
+          __syncwarp();
+        }
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db) {
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4_t(paged_at<D>(vt, 16 * warp + 8 * (mi >> 1) + rr, db * 16 + 8 * (mi & 1)), a0, a1, a2, a3);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) mma_bf16_16816(o[h][db], a0, a1, a2, a3, p[h][0], p[h][1]);
+        }
+        if (valid < 16) fence_proxy_async_smem();  // the zeroing writes precede the next TMA into the stage
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    if (!(flags & kTileLast)) continue;
+    // ---- join the warps: 1 .. NW - 1 hand theirs to warp 0 through shared memory
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) l[h][k] += __shfl_xor_sync(0xffffffffu, l[h][k], sh);
+    if (warp > 0) {
+      if (seg > 0 && !wait_warp(join_free, uint32_t((seg - 1) & 1))) return;
+      float* mo = merge + (warp - 1) * C::MERGE_FLOATS;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mo[((h * (D / 16) + db) * 4 + k) * 32 + lane] = o[h][db][k];
+        if (gid == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            mo[C::HEADS * D + 8 * h + 2 * tid + k] = m[h][k];
+            mo[C::HEADS * D + C::HEADS + 8 * h + 2 * tid + k] = l[h][k];
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join_full);
+    } else {
+      if (!wait_warp(join_full, uint32_t(seg & 1))) return;
+      const bool whole = flags & kTileWhole;
+      const size_t row0 = size_t(b) * a.Hq + size_t(g) * a.G;  // first query head row of the group
+      float* part = a.parts + size_t(2 * blockIdx.x + (flags & kTileStart ? 1 : 0)) * C::MERGE_FLOATS;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float f[C::NW][2], mx[2], lt[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int hd = C::HEADS * D + 8 * h + 2 * tid + k;
+          mx[k] = m[h][k];
+#pragma unroll
+          for (int w = 1; w < C::NW; ++w) mx[k] = fmaxf(mx[k], merge[(w - 1) * C::MERGE_FLOATS + hd]);
+          const float ref = mx[k] == -INFINITY ? 0.f : mx[k];
+          f[0][k] = ex2(m[h][k] - ref);
+          lt[k] = f[0][k] * l[h][k];
+#pragma unroll
+          for (int w = 1; w < C::NW; ++w) {
+            f[w][k] = ex2(merge[(w - 1) * C::MERGE_FLOATS + hd] - ref);
+            lt[k] = fmaf(f[w][k], merge[(w - 1) * C::MERGE_FLOATS + hd + C::HEADS], lt[k]);
+          }
+        }
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float v = o[h][db][k] * f[0][k & 1];
+#pragma unroll
+            for (int w = 1; w < C::NW; ++w)
+              v = fmaf(f[w][k & 1], merge[(w - 1) * C::MERGE_FLOATS + ((h * (D / 16) + db) * 4 + k) * 32 + lane], v);
+            const int head = 8 * h + 2 * tid + (k & 1), e = 16 * db + gid + 8 * (k >> 1);
+            if (!whole)
+              part[head * D + e] = v;
+            else if (head < a.G)
+              a.o[(row0 + head) * D + e] = __float2bfloat16_rn(lt[k & 1] != 0.f ? v / lt[k & 1] : 0.f);
+          }
+        if (gid == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int head = 8 * h + 2 * tid + k;
+            if (!whole) {
+              part[C::HEADS * D + head] = mx[k];
+              part[C::HEADS * D + C::HEADS + head] = lt[k];
+            } else if (head < a.G) {
+              a.lse[row0 + head] = lt[k] != 0.f ? mx[k] * 0.6931471805599453f + logf(lt[k]) : -INFINITY;
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join_free);
+    }
+    ++seg;
+  }
+}
+
+// Joins the parts of the (b, g) pairs that several CTAs shared, one block per query head row: with (m_s, l_s,
+// o_s) per part, M = max m_s, O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s, LSE = ln 2 M + ln of that sum. The
+// parts are taken in order, whatever order they were written in. Rows of sequences without tokens get 0 and
+// -inf here.
+constexpr int kJoinThreads = 128;
+
+template <int D, int NH>
+__global__ void __launch_bounds__(kJoinThreads)
+    decode_paged_join_kernel(const long long* head, const float* parts, __nv_bfloat16* __restrict__ o,
+                             float* __restrict__ lse, int Hkv, int G) {
+  using C = PagedCfg<D, NH>;
+  constexpr int NWARP = kJoinThreads / 32, EPL = D / 32;  // elements of d per lane
+  __shared__ float w[kPagedMaxCtas];
+  __shared__ float red[NWARP], acc[NWARP][D];
+  const int row = blockIdx.x, hd = row % G, g = row / G % Hkv, b = row / G / Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  const long long W = head[0], N = head[1], first = head[2 + b], nt = head[3 + b] - first;
+  if (nt <= 0) {
+    for (int e = threadIdx.x; e < D; e += kJoinThreads) o[size_t(row) * D + e] = __float2bfloat16_rn(0.f);
+    if (threadIdx.x == 0) lse[row] = -INFINITY;
+    return;
+  }
+  const long long base = first * Hkv + g * nt;  // the pair's tiles are base .. base + nt
+  // the CTA that holds tile x of the list: the smallest i with x < floor((i + 1) W / N)
+  const int c0 = int(((base + 1) * N - 1) / W), c1 = int(min(N - 1, ((base + nt) * N - 1) / W));
+  if (c0 >= c1) return;
+  const int n = c1 - c0 + 1;
+  // slot of part s: the first CTA's tiles start the pair (its second slot), the others' continue it
+  auto slot = [&](int s) -> const float* { return parts + size_t(2 * (c0 + s) + (s == 0 ? 1 : 0)) * C::MERGE_FLOATS; };
+  float mx = -INFINITY;
+  for (int s = threadIdx.x; s < n; s += kJoinThreads) {
+    w[s] = slot(s)[C::HEADS * D + hd];
+    mx = fmaxf(mx, w[s]);
+  }
+#pragma unroll
+  for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NWARP; ++i) mx = fmaxf(mx, red[i]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  __syncthreads();
+  float z = 0.f;
+  for (int s = threadIdx.x; s < n; s += kJoinThreads) {
+    const float f = ex2(w[s] - ref);
+    w[s] = f;
+    z = fmaf(f, slot(s)[C::HEADS * D + C::HEADS + hd], z);
+  }
+#pragma unroll
+  for (int sh = 16; sh > 0; sh >>= 1) z += __shfl_xor_sync(0xffffffffu, z, sh);
+  if (lane == 0) red[warp] = z;
+  __syncthreads();
+  z = 0.f;
+#pragma unroll
+  for (int i = 0; i < NWARP; ++i) z += red[i];
+  float v[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) v[e] = 0.f;
+#pragma unroll 4
+  for (int s = warp; s < n; s += NWARP) {
+    const float* po = slot(s) + hd * D + lane;
+    const float f = w[s];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) v[e] = fmaf(f, po[32 * e], v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) acc[warp][lane + 32 * e] = v[e];
+  __syncthreads();
+  const float inv = z != 0.f ? 1.f / z : 0.f;
+  for (int e = threadIdx.x; e < D; e += kJoinThreads) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < NWARP; ++i) x += acc[i][e];
+    o[size_t(row) * D + e] = __float2bfloat16_rn(x * inv);
+  }
+  if (threadIdx.x == 0) lse[row] = z != 0.f ? mx * 0.6931471805599453f + logf(z) : -INFINITY;
+}
+
+// Workspace: W, N and the tile counts, then the part slots.
+size_t paged_head_bytes(int B) { return (size_t(3 + B) * sizeof(long long) + 255) / 256 * 256; }
+
+template <int D, int NH>
+attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStream_t stream) {
+  using C = PagedCfg<D, NH>;
+  auto kernel = decode_paged_kernel<D, NH>;
+  const long long dims[4] = {D, a.Hkv, a.page_size, a.n_pages};
+  const int box[4] = {C::CE, 1, a.box, 1};
+  const unsigned swz = D >= 64 ? 128u : 0u;
+  CUtensorMap tmK, tmV;
+  if (!encode_map(&tmK, kp, 2, dims, box, swz) || !encode_map(&tmV, vp, 2, dims, box, swz)) return ATTN_ERR_CUDA;
+  if (ensure_dyn_smem(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES) != cudaSuccess) return ATTN_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  const int grid = C::CTAS * sms < kPagedMaxCtas ? C::CTAS * sms : kPagedMaxCtas;
+  kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tmK, tmV, a);
+  if (cudaPeekAtLastError() != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = dim3(unsigned(a.B) * unsigned(a.Hq));
+  lc.blockDim = dim3(kJoinThreads);
+  lc.stream = stream;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, decode_paged_join_kernel<D, NH>, static_cast<const long long*>(a.head),
+                         static_cast<const float*>(a.parts), a.o, a.lse, a.Hkv, a.G) != cudaSuccess)
+    return cudaGetLastError(), ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 // New rows into the pages of their sequences: pure copies. A block takes `rows` consecutive packed rows:
@@ -140,7 +673,8 @@ extern "C" {
 
 size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return 0;
-  return 16;
+  const size_t heads = Hq / Hkv <= 8 ? 8 : 16;
+  return paged_head_bytes(B) + 2 * size_t(kPagedMaxCtas) * heads * (size_t(d) + 2) * sizeof(float);
 }
 
 attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -161,29 +695,33 @@ attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* 
   if (workspace == nullptr || !is_aligned16(workspace) ||
       workspace_bytes < attn_decode_paged_workspace_bytes(B, Hq, Hkv, d))
     return ATTN_ERR_WORKSPACE;
-  const auto* qb = static_cast<const __nv_bfloat16*>(q);
-  const auto* kb = static_cast<const __nv_bfloat16*>(k_pages);
-  const auto* vb = static_cast<const __nv_bfloat16*>(v_pages);
-  auto* ob = static_cast<__nv_bfloat16*>(o);
-  const unsigned grid = unsigned(((long long)B * Hq + 3) / 4);
+  if ((long long)B * Hq > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+  PagedArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.table = page_table;
+  a.kv_lens = kv_lens;
+  a.n_pages = n_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.q_stride = q_stride;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.head = static_cast<long long*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + paged_head_bytes(B));
+  a.timeout_ns = kWaitLimitNs;
+  const bool wide = a.G > 8;
   switch (d) {
-    case 32:
-      decode_paged_simple_kernel<32><<<grid, 128, 0, stream>>>(qb, kb, vb, page_table, kv_lens, n_pages, page_size,
-                                                               max_pages, ob, lse, B, Hq, Hkv, q_stride, scale);
-      break;
-    case 64:
-      decode_paged_simple_kernel<64><<<grid, 128, 0, stream>>>(qb, kb, vb, page_table, kv_lens, n_pages, page_size,
-                                                               max_pages, ob, lse, B, Hq, Hkv, q_stride, scale);
-      break;
-    case 128:
-      decode_paged_simple_kernel<128><<<grid, 128, 0, stream>>>(qb, kb, vb, page_table, kv_lens, n_pages, page_size,
-                                                                max_pages, ob, lse, B, Hq, Hkv, q_stride, scale);
-      break;
-    default:
-      decode_paged_simple_kernel<256><<<grid, 128, 0, stream>>>(qb, kb, vb, page_table, kv_lens, n_pages, page_size,
-                                                                max_pages, ob, lse, B, Hq, Hkv, q_stride, scale);
+    case 32: return wide ? launch_paged<32, 2>(a, k_pages, v_pages, stream) : launch_paged<32, 1>(a, k_pages, v_pages, stream);
+    case 64: return wide ? launch_paged<64, 2>(a, k_pages, v_pages, stream) : launch_paged<64, 1>(a, k_pages, v_pages, stream);
+    case 128: return wide ? launch_paged<128, 2>(a, k_pages, v_pages, stream) : launch_paged<128, 1>(a, k_pages, v_pages, stream);
+    default: return wide ? launch_paged<256, 2>(a, k_pages, v_pages, stream) : launch_paged<256, 1>(a, k_pages, v_pages, stream);
   }
-  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : (cudaGetLastError(), ATTN_ERR_CUDA);
 }
 
 attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int32_t* cu, const int32_t* page_table,

@@ -154,26 +154,35 @@ def test_decode_bad_lengths_and_pages_are_clamped_and_flagged(lib):
     lens, Hq, Hkv, d, page = [40, 100], 4, 2, 64, 16
     kp, vp, table, kv_lens, kc, vc = make_cache(8500, lens, page, Hkv, d, fill=0.0)
     q = gpu(synth.normal_bf16(8500, synth.STREAM_Q, (2, Hq, d)))
-    good, _ = lib.attn_decode_paged(q, kp, vp, table, kv_lens)
+    O, _, bO, _ = decode_reference(host(q), kc, vc, lens, 1 / math.sqrt(d))
+
+    def other_row_is_right(o):
+        # (the other sequence's length moves the split, so its last bits may move)
+        assert_within(host(o)[1], O[1], bO[1], "the other sequence")
+
+    o, _ = lib.attn_decode_paged(q, kp, vp, table, kv_lens)
     assert lib.attn_get_last_error() == lib.ATTN_OK
+    other_row_is_right(o)
     low = kv_lens.clone()
     low[0] = -5
     o, lse = lib.attn_decode_paged(q, kp, vp, table, low)
     assert lib.attn_get_last_error() == lib.ATTN_ERR_INVALID_ARG
-    assert bool((o[0] == 0).all()) and bool(torch.isneginf(lse[0]).all()) and torch.equal(o[1], good[1])
+    assert bool((o[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
+    other_row_is_right(o)
     full = table.clone()
     full[0] = full[1]  # every entry of the row names a page
     high = kv_lens.clone()
     high[0] = 10 ** 9
     o, lse = lib.attn_decode_paged(q, kp, vp, full, high)
     assert lib.attn_get_last_error() == lib.ATTN_ERR_INVALID_ARG
-    assert torch.isfinite(o.float()).all() and torch.equal(o[1], good[1])
+    assert torch.isfinite(o.float()).all()
+    other_row_is_right(o)
     for wrong in (-1, kp.shape[0], 2 ** 31 - 1, -2 ** 31):
         t = table.clone()
         t[0, 1] = wrong
         o, _ = lib.attn_decode_paged(q, kp, vp, t, kv_lens)
         assert lib.attn_get_last_error() == lib.ATTN_ERR_INVALID_ARG
-        assert torch.equal(o[1], good[1])
+        other_row_is_right(o)
 
 
 def _append_plain(kp, vp, k_new, v_new, table, lens, new):
