@@ -29,9 +29,10 @@ __device__ __forceinline__ int page_in_pool(int p, int n_pages) {
 
 // ---------------------------------------------------------------------------------------------
 // Split kernel. The work of a call is the list of 64-token tiles of every (sequence b, kv head g), in that
-// order; CTA i of N takes the contiguous share [i W / N, (i + 1) W / N) of the W tiles. Every CTA so streams
-// the same number of bytes whatever the lengths are, and neither the grid nor the workspace depends on the
-// capacity of the page table. A share covers whole (b, g) pairs, whose output is written here, and at its ends
+// order, with PAIR_COST empty entries before each pair's tiles for what a pair costs by itself (its queries'
+// loads, joining the warps, the output). CTA i of N takes the contiguous share [i W / N, (i + 1) W / N) of the
+// W entries. Every CTA so has the same work whatever the lengths are, and neither the grid nor the workspace
+// depends on the capacity of the page table. A share covers whole (b, g) pairs, whose output is written here, and at its ends
 // parts of pairs that other CTAs share: those leave (m, l, unnormalised O) in a workspace slot, at most two per
 // CTA, and the join kernel below merges them.
 //
@@ -43,7 +44,7 @@ __device__ __forceinline__ int page_in_pool(int p, int n_pages) {
 // MMA with a token's two heads per lane; movmatrix transposes the bf16 P into the B operand.
 // ---------------------------------------------------------------------------------------------
 constexpr int kPagedMaxCtas = 320;   // most CTAs of a launch (two per SM; bounds the workspace)
-constexpr int kPagedMinTiles = 4;    // tiles of a share, at least (fewer CTAs for little work)
+constexpr int kPagedMinShare = 4;    // entries of a share, at least (fewer CTAs for little work)
 
 template <int D, int NH>
 struct PagedCfg {
@@ -55,9 +56,13 @@ struct PagedCfg {
   static constexpr int CHUNK_BYTES = TT * ROWB;
   static constexpr int TILE_BYTES = TT * D * 2;  // one K or V tile
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int PAIR_COST = D >= 128 ? 1 : 128 / D;  // entries of about 32 KB of traffic
   static constexpr int HEADS = 8 * NH;          // query heads of a group, padded
-  static constexpr int MERGE_FLOATS = HEADS * (D + 2);  // one warp's (O, m, l)
-  static constexpr int MERGE_BYTES = (NW - 1) * MERGE_FLOATS * 4;
+  static constexpr int PART_FLOATS = HEADS * (D + 2);  // a part in the workspace: O, m, l
+  // shared memory of the join: each warp's m and l, and for each quarter of O's fragments the other warps' values
+  static constexpr int QUARTER = D / 4 / NW;    // accumulator registers per head block, of D / 4
+  static constexpr int MERGE_FLOATS = NW * 2 * HEADS + NW * (NW - 1) * NH * QUARTER * 32;
+  static constexpr int MERGE_BYTES = MERGE_FLOATS * 4;
   static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
   static constexpr int SMEM_CAP = (CTAS == 1 ? 227 : 113) * 1024;
   static constexpr int FIT = (SMEM_CAP - 1024 - MERGE_BYTES - 512) / STAGE_BYTES;
@@ -79,6 +84,7 @@ enum : int {
   kTileLast = 2,    // last one
   kTileWhole = 4,   // the segment is the whole (b, g) pair: its output is final
   kTileStart = 8,   // the segment starts the pair (else it continues it)
+  kTileStop = 16,   // no tile: the share is done
 };
 
 struct PagedArgs {
@@ -92,8 +98,8 @@ struct PagedArgs {
   int B, Hq, Hkv, G;
   long long q_stride;
   float scale_log2;
-  long long* head;   // workspace: W, N, then the tiles before each sequence and all of them [B + 1]
-  float* parts;      // workspace: [2 * CTA + end] slots of HEADS x D (O), HEADS (m), HEADS (l)
+  long long* head;   // workspace: W, N, then the entries (of one kv head) before each sequence, and all [B + 1]
+  float* parts;      // workspace: [2 * CTA + end] slots of PART_FLOATS
   unsigned long long timeout_ns;
 };
 
@@ -131,16 +137,19 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
       reinterpret_cast<volatile PagedTile*>(smem + C::STAGES * C::STAGE_BYTES + C::MERGE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::MERGE_BYTES + 16 * C::STAGES);
   uint64_t* empty = full + C::STAGES;
-  uint64_t* join_full = empty + C::STAGES;  // one phase per segment: warps 1 .. NW - 1 left theirs in `merge`
-  uint64_t* join_free = join_full + 1;      // one phase per segment: warp 0 has read it
-  long long* s_base = reinterpret_cast<long long*>(join_free + 1);  // tiles before s_seq's
-  long long* s_warp = s_base + 1;                                   // [NW + 1] per-warp tile sums
+  uint64_t* join_full = empty + C::STAGES;  // one phase per segment: every warp left its parts in `merge`
+  uint64_t* join_free = join_full + 1;      // one phase per segment: every warp has read the others'
+  long long* s_base = reinterpret_cast<long long*>(join_free + 1);  // entries (of one kv head) before s_seq's
+  long long* s_warp = s_base + 1;                                   // [NW + 1] per-warp sums of entries
   volatile int* abort_flag = reinterpret_cast<volatile int*>(s_warp + C::NW + 1);
   volatile int* s_seq = abort_flag + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t T = a.timeout_ns;
   const long long cap = (long long)a.max_pages * a.page_size;
-  auto tiles_of = [&](int b) -> int { return int((paged_len(a.kv_lens, b, cap) + (long long)C::TT - 1) / C::TT); };
+  auto entries_of = [&](int b) -> int {  // tiles of a kv head of sequence b, and the pair's cost
+    const int L = paged_len(a.kv_lens, b, cap);
+    return L > 0 ? (L - 1) / C::TT + 1 + C::PAIR_COST : 0;
+  };
 
   pdl_launch();
   if (threadIdx.x == 0) {
@@ -148,19 +157,19 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], C::NW);
     }
-    mbar_init(join_full, C::NW - 1);
-    mbar_init(join_free, 1);
+    mbar_init(join_full, C::NW);
+    mbar_init(join_free, C::NW);
     *abort_flag = 0;
     *s_seq = a.B;
     fence_mbar_init();
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  // ---- this CTA's share: tiles before each thread's run of sequences, by a scan over the block
+  // ---- this CTA's share: entries before each thread's run of sequences, by a scan over the block
   const int per = (a.B + C::THREADS - 1) / C::THREADS;
   const int b_lo = min(a.B, int(threadIdx.x) * per), b_hi = min(a.B, b_lo + per);
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b);
+  for (int b = b_lo; b < b_hi; ++b) mine += entries_of(b);
   long long scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +185,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
     total += s_warp[w];
   }
   const long long W = total * a.Hkv;
-  const long long want = (W + kPagedMinTiles - 1) / kPagedMinTiles;
+  const long long want = (W + kPagedMinShare - 1) / kPagedMinShare;
   const long long N = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) {
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
     long long x = before;
     for (int b = b_lo; b < b_hi; ++b) {
       a.head[2 + b] = x;
-      x += tiles_of(b);
+      x += entries_of(b);
       if (b == a.B - 1) a.head[2 + a.B] = x;
     }
   }
@@ -196,7 +205,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
     long long x = before;
     int b = b_lo;
     for (; b < b_hi - 1; ++b) {
-      const int n = tiles_of(b);
+      const int n = entries_of(b);
       if (begin < (x + n) * a.Hkv) break;
       x += n;
     }
@@ -204,56 +213,58 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
     *s_base = x;
   }
   __syncthreads();
-  const int n_tiles = int(end - begin);
 
   if (warp == C::NW) {
     // ================================ TMA producer ================================
     const int subs = C::TT / a.box;  // boxes of a tile; lane k < subs loads box k
-    int b = *s_seq, L = 0, nt = 0, g = 0, t = 0;  // the tile to load next: tile t of the nt of (b, g)
+    int b = *s_seq, L = 0, n = 0, g = 0, t = 0;  // the tile to load next: tile t of (b, g), which has n entries
+    long long at = end;                          // its entry
     auto page_of = [&]() -> int {  // page of this lane's box of that tile, or -1 past the sequence's end
-      const long long tok = (long long)t * C::TT + lane * a.box;
-      if (lane >= subs || tok >= L) return -1;
-      return page_in_pool(__ldg(a.table + size_t(b) * a.max_pages + int(tok / a.page_size)), a.n_pages);
+      const unsigned tok = unsigned(t) * C::TT + lane * a.box;
+      if (lane >= subs || tok >= unsigned(L)) return -1;
+      return page_in_pool(__ldg(a.table + size_t(b) * a.max_pages + tok / unsigned(a.page_size)), a.n_pages);
     };
     int page = -1;
-    if (b < a.B) {
+    if (b < a.B && (n = entries_of(b)) > 0) {
       L = paged_len(a.kv_lens, b, cap);
-      nt = tiles_of(b);
       const long long off = begin - *s_base * a.Hkv;
-      if (nt > 0 && off >= 0 && off < (long long)nt * a.Hkv) {
-        g = int(off / nt);
-        t = int(off % nt);
+      if (off >= 0 && off < (long long)n * a.Hkv) {
+        g = int(off / n);
+        t = max(0, int(off % n) - C::PAIR_COST);
+        at = *s_base * a.Hkv + (long long)g * n + C::PAIR_COST + t;
         page = page_of();
       }
     }
     int t_first = t;  // first tile of the current segment
     int i = 0;        // tiles issued
     bool ok = true;
-    for (; i < n_tiles; ++i) {
-      if (t >= nt) {  // (only if kv_lens changed under the call)
-        if (lane == 0) *abort_flag = 1, atomicOr(&g_error_word, kErrBadLengthBit);
-        break;
-      }
+    while (at < end) {
+      const int nt = n - C::PAIR_COST;
       PagedTile now;
       now.b = b;
       now.g = g;
-      now.valid = int(min((long long)C::TT, L - (long long)t * C::TT));
-      now.flags = (t == t_first ? kTileFirst : 0) | (t + 1 == nt || i + 1 == n_tiles ? kTileLast : 0) |
+      now.valid = min(C::TT, L - t * C::TT);
+      now.flags = (t == t_first ? kTileFirst : 0) | (t + 1 == nt || at + 1 == end ? kTileLast : 0) |
                   (t_first == 0 ? kTileStart : 0) | (t_first == 0 && t + 1 == nt ? kTileWhole : 0);
-      const int row = int(((long long)t * C::TT + lane * a.box) % a.page_size), cur = page;
+      const int row = int((unsigned(t) * C::TT + lane * a.box) % unsigned(a.page_size)), cur = page;
       // the next tile and its pages, while the stage becomes free
-      if (i + 1 < n_tiles) {
+      ++at;
+      if (at < end) {
         if (++t == nt) {
           t = t_first = 0;
+          at += C::PAIR_COST;
           if (++g == a.Hkv) {
             g = 0;
-            for (++b; b < a.B; ++b)
-              if ((nt = tiles_of(b)) > 0) break;
-            L = b < a.B ? paged_len(a.kv_lens, b, cap) : 0;
-            if (b >= a.B) nt = 0;
+            n = 0;
+            while (++b < a.B && (n = entries_of(b)) == 0) {
+            }
+            if (b < a.B)
+              L = paged_len(a.kv_lens, b, cap);
+            else
+              at = end;  // (only if kv_lens changed under the call)
           }
         }
-        page = t < nt ? page_of() : -1;
+        page = at < end ? page_of() : -1;
       }
       const int st = i % C::STAGES;
       ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], uint32_t(((i / C::STAGES) & 1) ^ 1), abort_flag, T));
@@ -275,8 +286,13 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
           tma_load_4d(kt + C::TILE_BYTES + c * C::CHUNK_BYTES, &tmV, &full[st], c * C::CE, now.g, row, cur);
         }
       }
+      ++i;
     }
-    if (i < n_tiles) ok = false;
+    const int st = i % C::STAGES;
+    if (ok && lane == 0 && (ok = mbar_wait(&empty[st], uint32_t(((i / C::STAGES) & 1) ^ 1), abort_flag, T))) {
+      tile_of[st].flags = kTileStop;
+      mbar_arrive(&full[st]);
+    }
     if (!ok && lane == 0) {
       // gave up: let the copies in flight land before the CTA exits
       for (int st = 0; st < C::STAGES; ++st) {
@@ -299,10 +315,11 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
   auto wait_warp = [&](uint64_t* bar, uint32_t ph) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag, T));
   };
-  for (int i = 0; i < n_tiles; ++i) {
+  for (int i = 0;; ++i) {
     const int st = i % C::STAGES;
     if (!wait_warp(&full[st], uint32_t((i / C::STAGES) & 1))) return;
     const int b = tile_of[st].b, g = tile_of[st].g, flags = tile_of[st].flags;
+    if (flags & kTileStop) return;
     const int valid = tile_of[st].valid - 16 * warp;  // of this warp's 16 tokens
     if (flags & kTileFirst) {
 #pragma unroll
@@ -407,94 +424,105 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
       if (lane == 0) mbar_arrive(&empty[st]);
     }
     if (!(flags & kTileLast)) continue;
-    // ---- join the warps: 1 .. NW - 1 hand theirs to warp 0 through shared memory
+    // ---- join the warps: each takes a quarter of O's fragments and leaves the others' quarters to them
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[h][k] += __shfl_xor_sync(0xffffffffu, l[h][k], sh);
-    if (warp > 0) {
-      if (seg > 0 && !wait_warp(join_free, uint32_t((seg - 1) & 1))) return;
-      float* mo = merge + (warp - 1) * C::MERGE_FLOATS;
+    if (seg > 0 && !wait_warp(join_free, uint32_t((seg - 1) & 1))) return;
+    float* ml = merge;                                // [NW][2][HEADS]: m, l
+    float* mo = merge + C::NW * 2 * C::HEADS + lane;  // [to][from][h][register][lane], from != to
+    if (gid == 0) {
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-#pragma unroll
-        for (int db = 0; db < D / 16; ++db)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mo[((h * (D / 16) + db) * 4 + k) * 32 + lane] = o[h][db][k];
-        if (gid == 0) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            mo[C::HEADS * D + 8 * h + 2 * tid + k] = m[h][k];
-            mo[C::HEADS * D + C::HEADS + 8 * h + 2 * tid + k] = l[h][k];
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(join_full);
-    } else {
-      if (!wait_warp(join_full, uint32_t(seg & 1))) return;
-      const bool whole = flags & kTileWhole;
-      const size_t row0 = size_t(b) * a.Hq + size_t(g) * a.G;  // first query head row of the group
-      float* part = a.parts + size_t(2 * blockIdx.x + (flags & kTileStart ? 1 : 0)) * C::MERGE_FLOATS;
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        float f[C::NW][2], mx[2], lt[2];
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int hd = C::HEADS * D + 8 * h + 2 * tid + k;
-          mx[k] = m[h][k];
-#pragma unroll
-          for (int w = 1; w < C::NW; ++w) mx[k] = fmaxf(mx[k], merge[(w - 1) * C::MERGE_FLOATS + hd]);
-          const float ref = mx[k] == -INFINITY ? 0.f : mx[k];
-          f[0][k] = ex2(m[h][k] - ref);
-          lt[k] = f[0][k] * l[h][k];
-#pragma unroll
-          for (int w = 1; w < C::NW; ++w) {
-            f[w][k] = ex2(merge[(w - 1) * C::MERGE_FLOATS + hd] - ref);
-            lt[k] = fmaf(f[w][k], merge[(w - 1) * C::MERGE_FLOATS + hd + C::HEADS], lt[k]);
-          }
+          ml[warp * 2 * C::HEADS + 8 * h + 2 * tid + k] = m[h][k];
+          ml[(warp * 2 + 1) * C::HEADS + 8 * h + 2 * tid + k] = l[h][k];
         }
+    }
 #pragma unroll
-        for (int db = 0; db < D / 16; ++db)
+    for (int to = 0; to < C::NW; ++to) {
+      if (to == warp) continue;
+      float* dst = mo + (to * (C::NW - 1) + (warp < to ? warp : warp - 1)) * NH * C::QUARTER * 32;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v = o[h][db][k] * f[0][k & 1];
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int w = 1; w < C::NW; ++w)
-              v = fmaf(f[w][k & 1], merge[(w - 1) * C::MERGE_FLOATS + ((h * (D / 16) + db) * 4 + k) * 32 + lane], v);
-            const int head = 8 * h + 2 * tid + (k & 1), e = 16 * db + gid + 8 * (k >> 1);
-            if (!whole)
-              part[head * D + e] = v;
-            else if (head < a.G)
-              a.o[(row0 + head) * D + e] = __float2bfloat16_rn(lt[k & 1] != 0.f ? v / lt[k & 1] : 0.f);
-          }
-        if (gid == 0) {
+        for (int r = 0; r < C::QUARTER; ++r) {
+          const int e = to * C::QUARTER + r;
+          dst[(h * C::QUARTER + r) * 32] = o[h][e >> 2][e & 3];
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(join_full);
+    if (!wait_warp(join_full, uint32_t(seg & 1))) return;
+    const bool whole = flags & kTileWhole;
+    const size_t row0 = size_t(b) * a.Hq + size_t(g) * a.G;  // first query head row of the group
+    float* part = a.parts + size_t(2 * blockIdx.x + (flags & kTileStart ? 1 : 0)) * C::PART_FLOATS;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int head = 8 * h + 2 * tid + k;
-            if (!whole) {
-              part[C::HEADS * D + head] = mx[k];
-              part[C::HEADS * D + C::HEADS + head] = lt[k];
-            } else if (head < a.G) {
-              a.lse[row0 + head] = lt[k] != 0.f ? mx[k] * 0.6931471805599453f + logf(lt[k]) : -INFINITY;
-            }
+    for (int h = 0; h < NH; ++h) {
+      float f[C::NW][2], mx[2], lt[2], inv[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float* mh = ml + 8 * h + 2 * tid + k;
+        mx[k] = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) mx[k] = fmaxf(mx[k], mh[w * 2 * C::HEADS]);
+        const float ref = mx[k] == -INFINITY ? 0.f : mx[k];
+        lt[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          f[w][k] = ex2(mh[w * 2 * C::HEADS] - ref);
+          lt[k] = fmaf(f[w][k], mh[(w * 2 + 1) * C::HEADS], lt[k]);
+        }
+        inv[k] = whole ? (lt[k] != 0.f ? 1.f / lt[k] : 0.f) : 1.f;
+      }
+#pragma unroll
+      for (int to = 0; to < C::NW; ++to) {  // (a register's index has to be a constant)
+        if (to != warp) continue;
+        const float* src = mo + to * (C::NW - 1) * NH * C::QUARTER * 32;
+#pragma unroll
+        for (int r = 0; r < C::QUARTER; ++r) {
+          const int e = to * C::QUARTER + r, k = e & 1;
+          float v = o[h][e >> 2][e & 3] * f[to][k];
+#pragma unroll
+          for (int w = 0; w < C::NW; ++w)
+            if (w != to)
+              v = fmaf(f[w][k], src[((w < to ? w : w - 1) * NH + h) * C::QUARTER * 32 + r * 32], v);
+          const int head = 8 * h + 2 * tid + k, d = 16 * (e >> 2) + gid + 8 * ((e >> 1) & 1);
+          if (!whole)
+            part[head * D + d] = v;
+          else if (head < a.G)
+            a.o[(row0 + head) * D + d] = __float2bfloat16_rn(v * inv[k]);
+        }
+      }
+      if (warp == 0 && gid == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int head = 8 * h + 2 * tid + k;
+          if (!whole) {
+            part[C::HEADS * D + head] = mx[k];
+            part[C::HEADS * D + C::HEADS + head] = lt[k];
+          } else if (head < a.G) {
+            a.lse[row0 + head] = lt[k] != 0.f ? mx[k] * 0.6931471805599453f + logf(lt[k]) : -INFINITY;
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(join_free);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(join_free);
     ++seg;
   }
 }
 
 // Joins the parts of the (b, g) pairs that several CTAs shared, one block per query head row: with (m_s, l_s,
-// o_s) per part, M = max m_s, O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s, LSE = ln 2 M + ln of that sum. The
-// parts are taken in order, whatever order they were written in. Rows of sequences without tokens get 0 and
-// -inf here.
-constexpr int kJoinThreads = 128;
+// o_s) per part, M = max m_s, O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s, LSE = ln 2 M + ln of that sum. Each
+// warp takes every NWARP-th part with a running maximum (one pass: all loads of a part are independent), then
+// the warps are merged; the order of the sums does not depend on timing. Rows of sequences without tokens get
+// 0 and -inf here.
+constexpr int kJoinThreads = 256;
 
 template <int D, int NH>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -502,74 +530,65 @@ __global__ void __launch_bounds__(kJoinThreads)
                              float* __restrict__ lse, int Hkv, int G) {
   using C = PagedCfg<D, NH>;
   constexpr int NWARP = kJoinThreads / 32, EPL = D / 32;  // elements of d per lane
-  __shared__ float w[kPagedMaxCtas];
-  __shared__ float red[NWARP], acc[NWARP][D];
+  __shared__ float sm[NWARP], sl[NWARP], acc[NWARP][D];
   const int row = blockIdx.x, hd = row % G, g = row / G % Hkv, b = row / G / Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const long long W = head[0], N = head[1], first = head[2 + b], nt = head[3 + b] - first;
-  if (nt <= 0) {
+  const long long W = head[0], N = head[1], first = head[2 + b], n = head[3 + b] - first;
+  if (n <= 0) {
     for (int e = threadIdx.x; e < D; e += kJoinThreads) o[size_t(row) * D + e] = __float2bfloat16_rn(0.f);
     if (threadIdx.x == 0) lse[row] = -INFINITY;
     return;
   }
-  const long long base = first * Hkv + g * nt;  // the pair's tiles are base .. base + nt
-  // the CTA that holds tile x of the list: the smallest i with x < floor((i + 1) W / N)
-  const int c0 = int(((base + 1) * N - 1) / W), c1 = int(min(N - 1, ((base + nt) * N - 1) / W));
+  // the CTA that holds entry x of the list: the smallest i with x < floor((i + 1) W / N)
+  const long long x0 = first * Hkv + g * n + C::PAIR_COST, x1 = first * Hkv + (g + 1) * n - 1;  // first, last tile
+  const int c0 = int(((x0 + 1) * N - 1) / W), c1 = int(min(N - 1, ((x1 + 1) * N - 1) / W));
   if (c0 >= c1) return;
-  const int n = c1 - c0 + 1;
-  // slot of part s: the first CTA's tiles start the pair (its second slot), the others' continue it
-  auto slot = [&](int s) -> const float* { return parts + size_t(2 * (c0 + s) + (s == 0 ? 1 : 0)) * C::MERGE_FLOATS; };
-  float mx = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += kJoinThreads) {
-    w[s] = slot(s)[C::HEADS * D + hd];
-    mx = fmaxf(mx, w[s]);
-  }
-#pragma unroll
-  for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NWARP; ++i) mx = fmaxf(mx, red[i]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  __syncthreads();
-  float z = 0.f;
-  for (int s = threadIdx.x; s < n; s += kJoinThreads) {
-    const float f = ex2(w[s] - ref);
-    w[s] = f;
-    z = fmaf(f, slot(s)[C::HEADS * D + C::HEADS + hd], z);
-  }
-#pragma unroll
-  for (int sh = 16; sh > 0; sh >>= 1) z += __shfl_xor_sync(0xffffffffu, z, sh);
-  if (lane == 0) red[warp] = z;
-  __syncthreads();
-  z = 0.f;
-#pragma unroll
-  for (int i = 0; i < NWARP; ++i) z += red[i];
-  float v[EPL];
+  float m = -INFINITY, l = 0.f, v[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) v[e] = 0.f;
 #pragma unroll 4
-  for (int s = warp; s < n; s += NWARP) {
-    const float* po = slot(s) + hd * D + lane;
-    const float f = w[s];
+  for (int c = c0 + warp; c <= c1; c += NWARP) {
+    // the first CTA's tiles start the pair (its second slot), the others' continue it
+    const float* p = parts + size_t(2 * c + (c == c0 ? 1 : 0)) * C::PART_FLOATS;
+    const float pm = p[C::HEADS * D + hd], pl = p[C::HEADS * D + C::HEADS + hd];
+    float x[EPL];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) v[e] = fmaf(f, po[32 * e], v[e]);
+    for (int e = 0; e < EPL; ++e) x[e] = p[hd * D + lane + 32 * e];
+    const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
+    const float fo = ex2(m - ref), fp = ex2(pm - ref);
+    m = mn;
+    l = fmaf(fp, pl, l * fo);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) v[e] = fmaf(fp, x[e], v[e] * fo);
+  }
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
   }
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[warp][lane + 32 * e] = v[e];
   __syncthreads();
+  float mx = -INFINITY, z = 0.f, f[NWARP];
+#pragma unroll
+  for (int w = 0; w < NWARP; ++w) mx = fmaxf(mx, sm[w]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+  for (int w = 0; w < NWARP; ++w) {
+    f[w] = ex2(sm[w] - ref);
+    z = fmaf(f[w], sl[w], z);
+  }
   const float inv = z != 0.f ? 1.f / z : 0.f;
   for (int e = threadIdx.x; e < D; e += kJoinThreads) {
     float x = 0.f;
 #pragma unroll
-    for (int i = 0; i < NWARP; ++i) x += acc[i][e];
+    for (int w = 0; w < NWARP; ++w) x = fmaf(f[w], acc[w][e], x);
     o[size_t(row) * D + e] = __float2bfloat16_rn(x * inv);
   }
   if (threadIdx.x == 0) lse[row] = z != 0.f ? mx * 0.6931471805599453f + logf(z) : -INFINITY;
 }
 
-// Workspace: W, N and the tile counts, then the part slots.
+// Workspace: W, N and the entry counts, then the part slots.
 size_t paged_head_bytes(int B) { return (size_t(3 + B) * sizeof(long long) + 255) / 256 * 256; }
 
 template <int D, int NH>
