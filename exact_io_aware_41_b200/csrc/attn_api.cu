@@ -74,13 +74,15 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 }
 
 // A 4-d tiled TMA map: dims[0] innermost (contiguous), dims[i] elements of elem_bytes each, dense
-// strides; box[] elements per dimension; swizzle 128, 64 or 0 bytes.
+// strides (row_stride, if not 0, between the indices of dims[2]); box[] elements per dimension; swizzle
+// 128, 64 or 0 bytes.
 static bool encode_map_uncached(CUtensorMap* map, const void* base, int elem_bytes, const long long* dims,
-                                const int* box, unsigned swizzle_bytes) {
+                                const int* box, unsigned swizzle_bytes, long long row_stride) {
   auto fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t gd[4] = {cuuint64_t(dims[0]), cuuint64_t(dims[1]), cuuint64_t(dims[2]), cuuint64_t(dims[3])};
-  const cuuint64_t gs[3] = {gd[0] * elem_bytes, gd[0] * gd[1] * elem_bytes, gd[0] * gd[1] * gd[2] * elem_bytes};
+  const cuuint64_t row = cuuint64_t(row_stride ? row_stride : dims[0] * dims[1]) * elem_bytes;
+  const cuuint64_t gs[3] = {gd[0] * elem_bytes, row, row * gd[2]};
   const cuuint32_t bx[4] = {cuuint32_t(box[0]), cuuint32_t(box[1]), cuuint32_t(box[2]), cuuint32_t(box[3])};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   const CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
@@ -103,8 +105,9 @@ struct MapKey {
   long long dims[4];
   int box[4];
   unsigned swizzle;
+  long long row_stride;
   bool operator==(const MapKey& o) const {
-    if (base != o.base || elem_bytes != o.elem_bytes || swizzle != o.swizzle) return false;
+    if (base != o.base || elem_bytes != o.elem_bytes || swizzle != o.swizzle || row_stride != o.row_stride) return false;
     for (int i = 0; i < 4; ++i)
       if (dims[i] != o.dims[i] || box[i] != o.box[i]) return false;
     return true;
@@ -125,8 +128,9 @@ MapCache& map_cache() {
 }  // namespace
 
 bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long long* dims, const int* box,
-                unsigned swizzle_bytes) {
-  MapKey k{base, elem_bytes, {dims[0], dims[1], dims[2], dims[3]}, {box[0], box[1], box[2], box[3]}, swizzle_bytes};
+                unsigned swizzle_bytes, long long row_stride) {
+  MapKey k{base, elem_bytes, {dims[0], dims[1], dims[2], dims[3]}, {box[0], box[1], box[2], box[3]}, swizzle_bytes,
+           row_stride};
   MapCache& c = map_cache();
   std::lock_guard<std::mutex> lock(c.mu);
   for (int i = 0; i < kMapCacheSize; ++i) {
@@ -135,7 +139,7 @@ bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long l
       return true;
     }
   }
-  if (!encode_map_uncached(map, base, elem_bytes, dims, box, swizzle_bytes)) return false;
+  if (!encode_map_uncached(map, base, elem_bytes, dims, box, swizzle_bytes, row_stride)) return false;
   const int slot = c.next;
   c.next = (c.next + 1) % kMapCacheSize;
   c.key[slot] = k;
@@ -145,10 +149,10 @@ bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long l
 }
 
 bool encode_tile_map(CUtensorMap* map, const void* base, int d, int heads, int rows, int outer, int box_cols,
-                     int box_rows, unsigned swizzle_bytes) {
+                     int box_rows, unsigned swizzle_bytes, long long row_stride) {
   const long long dims[4] = {d, heads, rows, outer};
   const int box[4] = {box_cols, 1, box_rows, 1};
-  return encode_map(map, base, 2, dims, box, swizzle_bytes);
+  return encode_map(map, base, 2, dims, box, swizzle_bytes, row_stride);
 }
 
 namespace {
@@ -387,7 +391,7 @@ const char* attn_kernel_name(int which) {
     case 1: return "attn::decode_split_tc_kernel<D,G> (d <= 128), attn::decode_split_kernel<D,G> (d = 256)";
     case 2: return "attn::decode_combine_kernel<D>";
     case 3: return "attn::attn_bwd_pre_kernel, attn::attn_bwd_kernel, attn::attn_bwd_post_kernel";
-    case 4: return "attn::varlen_fwd_simple_kernel<D>";
+    case 4: return "attn::varlen_plan_kernel, attn::attn_fwd_kernel<D, F8, PAIR, VL>";
     case 5: return "attn::decode_paged_kernel<D, NH>, attn::decode_paged_join_kernel<D, NH>";
     case 6: return "attn::cache_append_kernel";
   }

@@ -132,9 +132,9 @@ struct FwdCfg {
   static constexpr int TMEM_COLS = 512;
   static_assert(2 * BN + NQT * D + (SEP_P ? NQT * BN / 2 : 0) <= TMEM_COLS, "tensor memory budget");
   // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_done, o_final[2], drain,
-  // s_free[2], p_free[2], sched_full[SCHED], sched_empty[SCHED]
+  // s_free[2], p_free[2], sched_full[SCHED], sched_empty[SCHED], v_land, v_clean
   static constexpr int SCHED = 4;  // units the producer may claim ahead of the consumers
-  static constexpr int NBARS = 2 + 2 * STAGES + 2 + 2 + 1 + 2 + 1 + 2 + 2 + 2 * SCHED;
+  static constexpr int NBARS = 2 + 2 * STAGES + 2 + 2 + 1 + 2 + 1 + 2 + 2 + 2 * SCHED + 2;
   static constexpr int SCHED_CONSUMERS = 1 + 4 * NSMWG;  // MMA thread + one arrival per softmax warp
   static constexpr int SMEM_DATA = NQT * Q_TILE_BYTES + STAGES * KV_TILE_BYTES;
   // Pad small-d configurations so only one CTA (and one 512-column TMEM allocation) fits per SM.
@@ -171,11 +171,35 @@ struct Unit {
   int b, h, q0;
   int n_tiles;   // K/V tiles the unit streams (the last query tile's count)
   int n_tile0;   // K/V tiles the first query tile needs (fewer when the last one is above its diagonal)
+  // packed sequences (q0 is a packed row; query rows count from it): queries and keys of the unit's sequence,
+  // packed row of its first key
+  int nq, nkv, k_row;
 };
 
-template <int D, bool PAIR>
+// VL: the units are the planned blocks of all sequences (heaviest first), every query head of a block in
+// turn, so that the heads of a group read the same K/V at about the same time.
+template <int D, bool PAIR, bool VL>
 __device__ __forceinline__ Unit unit_at(const FwdArgs& a, int lin) {
   using C = FwdCfg<D, false, PAIR>;
+  if constexpr (VL) {
+    const int4 r = *reinterpret_cast<const int4*>(a.var_units + lin / a.Hq);
+    Unit u;
+    u.b = 0;
+    u.h = lin % a.Hq;
+    u.q0 = r.x;
+    u.nq = r.y;
+    u.k_row = r.z;
+    u.nkv = r.w;
+    const int diag = u.nkv - u.nq;  // key j visible to the block's row i iff j <= i + diag
+    const int end = a.causal ? min(u.nkv, min(C::UNIT_ROWS, u.nq) + diag) : u.nkv;
+    u.n_tiles = end > 0 ? (end + C::BN - 1) / C::BN : 0;
+    u.n_tile0 = u.n_tiles;
+    if (C::NQT == 2 && a.causal) {
+      const int end0 = min(u.nkv, min(C::BM, u.nq) + diag);
+      u.n_tile0 = end0 > 0 ? (end0 + C::BN - 1) / C::BN : 0;
+    }
+    return u;
+  }
   const int BH = a.B * a.Hq;
   const int per_group = a.heads_per_group * a.n_qblk;
   const int grp = lin / per_group;
@@ -201,7 +225,7 @@ __device__ __forceinline__ Unit unit_at(const FwdArgs& a, int lin) {
   return u;
 }
 
-template <int D, bool F8, bool PAIR>
+template <int D, bool F8, bool PAIR, bool VL>
 __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const FwdArgs args) {
@@ -224,15 +248,18 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   uint64_t* p_free = s_free + 2;            // [tile] separate P: the PV reading the P buffer is done
   uint64_t* sched_full = p_free + 2;        // [SCHED] the producer wrote the k-th unit index
   uint64_t* sched_empty = sched_full + C::SCHED;  // [SCHED] every role read it
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sched_empty + C::SCHED);
+  // packed sequences, one phase per unit whose last tile holds the end of its sequence: the tile's V has landed
+  // (the MMA thread saw it) / its tail rows are zero
+  uint64_t* v_land = sched_empty + C::SCHED;
+  uint64_t* v_clean = v_land + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(v_clean + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* sched_unit = reinterpret_cast<volatile int*>(tmem_holder + 2);  // [SCHED]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint64_t T = args.timeout_ns;
-  const int total_units = args.B * args.Hq * args.n_qblk;
-  const int diag = args.Nkv - args.Nq;  // key j visible to query i iff j <= i + diag
+  int total_units = VL ? 0 : args.B * args.Hq * args.n_qblk;
   // CTA pair: rank 0 (the leader) issues the MMAs of both; barriers that the MMAs, the TMA copies
   // of both CTAs or the softmax warps of both CTAs feed live in the leader's shared memory
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -256,8 +283,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
     mbar_init(drain, 1);
     for (int i = 0; i < C::SCHED; ++i) {
       mbar_init(&sched_full[i], 1);
-      mbar_init(&sched_empty[i], C::SCHED_CONSUMERS);
+      mbar_init(&sched_empty[i], C::SCHED_CONSUMERS + (VL ? 1 : 0));  // (VL: the tail warp too)
     }
+    mbar_init(v_land, 1);
+    mbar_init(v_clean, C::CTAS);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -281,6 +310,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   if (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  if constexpr (VL) {
+    pdl_wait();  // the plan, a kernel of its own, is in memory
+    total_units = *args.var_count * args.Hq;
+  }
   // With two softmax warpgroups the 128 control threads give registers to the 256 softmax threads:
   // 128 * 104 + 256 * 192 = 62464 <= 384 * 168 (the launch allocation). Each role changes its budget
   // at the top of its own branch so the new limit covers all of that role's code.
@@ -317,10 +350,13 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   };
   // O += P V over the tile's keys: A = P (bf16, in TMEM over S), B = V tile read MN-major (N = d),
   // k-steps of 16 keys.
-  auto issue_pv = [&](int o_col, int p_col, int stage, bool accumulate) {
+  // keys: those of the tile that exist (packed sequences: the k-steps past a sequence's end are left out, so
+  // that only the last step's rows have to be zero behind it).
+  auto issue_pv = [&](int o_col, int p_col, int stage, bool accumulate, int keys) {
     const uint64_t b0 = dV + uint64_t((stage * C::KV_TILE_BYTES) >> 4);
 #pragma unroll
     for (int kk = 0; kk < C::BN / C::KSTEP; ++kk) {
+      if (VL && kk * C::KSTEP >= keys) break;
       // A = P: KSTEP keys = 8 TMEM columns in both forms; B: the next KSTEP rows of V (MN-major) or
       // the next 32 bytes of each transposed-V row (K-major)
       if (PAIR)
@@ -388,13 +424,13 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
             ok = false;
             break;
           }
-          const unsigned claimed = atomicAdd(&g_sched_next[args.sched_slot], 1u);
+          const unsigned claimed = atomicAdd(VL ? args.var_claim : &g_sched_next[args.sched_slot], 1u);
           lin = claimed < unsigned(total_units) ? int(claimed) : -1;
           sched_unit[slot] = lin;
           mbar_arrive(&sched_full[slot]);
         }
         if (lin < 0) break;
-        const Unit un = unit_at<D, PAIR>(args, lin);
+        const Unit un = unit_at<D, PAIR, VL>(args, lin);
         if (un.n_tiles == 0) continue;
         const int g = un.h / args.group;
         // Q of the previous unit must be consumed by all its QK MMAs before it is overwritten
@@ -422,6 +458,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
                           un.q0 + qt * C::BM, un.b);
         }
         ++qc;
+        const int k_row = VL ? un.k_row : 0;
         for (int j = 0; j < un.n_tiles && ok; ++j) {
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++pos) {
@@ -440,12 +477,12 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < C::NCHUNK; ++c)
                   tma_load_4d_pair(dst + c * C::K_CHUNK_BYTES, &tmK, bar_l, c * C::CHUNK, g,
-                                   j * C::BN + int(rank) * C::K_ROWS, un.b);
+                                   k_row + j * C::BN + int(rank) * C::K_ROWS, un.b);
               } else {
 #pragma unroll
                 for (int c = 0; c < C::V_COLS / C::CHUNK; ++c)
                   tma_load_4d_pair(dst + c * C::V_CHUNK_BYTES, &tmV, bar_l, int(rank) * C::V_COLS + c * C::CHUNK, g,
-                                   j * C::BN, un.b);
+                                   k_row + j * C::BN, un.b);
               }
               continue;
             }
@@ -458,7 +495,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
 #pragma unroll
               for (int c = 0; c < C::NCHUNK; ++c)
                 tma_load_4d(sKV + s * C::KV_TILE_BYTES + c * C::K_CHUNK_BYTES, m, &kv_full[s], c * C::CHUNK, g,
-                            j * C::BN, un.b);
+                            k_row + j * C::BN, un.b);
             }
           }
         }
@@ -488,15 +525,36 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
       int pc[2] = {0, 0};  // P tiles consumed per slot (phase of p_full)
       int qk_cnt[2] = {0, 0};  // separate P: S tiles issued per query tile (phase of s_free)
       int t_run = 0;  // single-tile path: S tiles issued so far (slot = t_run & 1)
+      int clean_cnt = 0;      // packed sequences: cut-off tiles so far (phase of v_clean)
       for (int k = 0; ok; ++k) {
         const int lin = PAIR ? pair_unit(k) : next_unit(k, false);
         if (lin < 0) break;
-        const Unit un = unit_at<D, PAIR>(args, lin);
+        const Unit un = unit_at<D, PAIR, VL>(args, lin);
         const int n = un.n_tiles;
         if (n == 0) continue;
         ok = wait_x(q_full, qc & 1);
         ++qc;
         const int base = pos;  // K_j at base + 2j, V_j at base + 2j + 1
+        // Packed sequences: keys of the last tile, if the sequence ends inside it. Its V tile goes to the tail
+        // warp (of both CTAs of a pair) when it has landed, which works while the softmax does, and its PV
+        // products wait for that (once per unit) and take those keys only.
+        const int cut = VL ? un.nkv - (n - 1) * C::BN : C::BN;
+        bool tail_out = false;
+        auto announce_tail = [&](int j) {
+          if (!VL || j + 1 < n || cut >= C::BN) return;
+          if (PAIR) mbar_arrive_release_cluster(mapa_shared(v_land, 1));
+          mbar_arrive(v_land);
+          tail_out = true;
+        };
+        auto pv_keys = [&](int j) -> int {
+          if (!VL || j + 1 < n || cut >= C::BN) return C::BN;
+          if (tail_out) {
+            ok = wait_x(v_clean, uint32_t(clean_cnt & 1));
+            ++clean_cnt;
+            tail_out = false;
+          }
+          return cut;
+        };
         if (C::SEP_P) {
           // Two query tiles, P in buffers of its own. QK(t, j+1) may overwrite S once the softmax has
           // read S(t, j) (s_free); PV(t, j) reads P(t, j) once it is in place (p_full) and frees the
@@ -522,6 +580,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
             const int pv_pos = base + 2 * j + 1, pk_pos = base + 2 * j + 2;
             const bool nxt = j + 1 < n;
             ok = wait_x(&kv_full[kv_slot(pv_pos)], kv_phase(pv_pos));
+            if (ok) announce_tail(j);
             if (ok && nxt) ok = wait_x(&kv_full[kv_slot(pk_pos)], kv_phase(pk_pos));
 #pragma unroll
             for (int qt = 0; qt < 2; ++qt)
@@ -532,8 +591,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
               ok = wait_x(&p_full[qt], pc[qt] & 1);
               if (!ok) break;
               ++pc[qt];
+              const int keys = pv_keys(j);
+              if (!ok) break;
               tc_fence_after();
-              issue_pv(qt ? C::O_COL1 : C::O_COL0, qt ? C::P_COL1 : C::P_COL0, kv_slot(pv_pos), j > 0);
+              issue_pv(qt ? C::O_COL1 : C::O_COL0, qt ? C::P_COL1 : C::P_COL0, kv_slot(pv_pos), j > 0, keys);
               commit(&p_free[qt]);
               if (qt == 0 && j == nt[0] - 1 && nt[0] < n) commit(&o_final[0]);  // see below
             }
@@ -561,6 +622,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
             const int pv_pos = base + 2 * j + 1, pk_pos = base + 2 * j + 2;
             const bool nxt = j + 1 < n;
             ok = wait_x(&kv_full[kv_slot(pv_pos)], kv_phase(pv_pos));
+            if (ok) announce_tail(j);
             if (ok && nxt) ok = wait_x(&kv_full[kv_slot(pk_pos)], kv_phase(pk_pos));
 #pragma unroll
             for (int qt = 0; qt < 2; ++qt) {
@@ -570,8 +632,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
               ok = wait_x(&p_full[qt], pc[qt] & 1);
               if (!ok) break;
               ++pc[qt];
+              const int keys = pv_keys(j);
+              if (!ok) break;
               tc_fence_after();
-              issue_pv(qt ? C::O_COL1 : C::O_COL0, s_col, kv_slot(pv_pos), j > 0);
+              issue_pv(qt ? C::O_COL1 : C::O_COL0, s_col, kv_slot(pv_pos), j > 0, keys);
               if (qt == 0 && j == nt[0] - 1 && nt[0] < n) commit(&o_final[0]);  // see below
               // P of this tile is consumed by the PV MMAs above before this QK overwrites the slot:
               // MMAs issued by one thread execute in issue order.
@@ -602,10 +666,13 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
             const int slot = t & 1;
             const int s_col = slot ? C::S_COL1 : C::S_COL0;
             ok = wait_x(&kv_full[kv_slot(base + 2 * j + 1)], kv_phase(base + 2 * j + 1));
+            if (ok) announce_tail(j);
             if (ok) ok = wait_x(&p_full[slot], (t >> 1) & 1);
             if (!ok) break;
+            const int keys = pv_keys(j);
+            if (!ok) break;
             tc_fence_after();
-            issue_pv(C::O_COL0, s_col, kv_slot(base + 2 * j + 1), j > 0);
+            issue_pv(C::O_COL0, s_col, kv_slot(base + 2 * j + 1), j > 0, keys);
             commit(o_done);
             commit(&kv_empty[kv_slot(base + 2 * j + 1)]);
             if (j + 2 < n) {
@@ -641,6 +708,47 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
     __syncwarp();
   } else if (warp < 4) {
     if (kSplitRegs) regs_dec<C::CTRL_REGS>();
+    if (VL && warp == 3) {
+      // ================================ tail rows ================================
+      // Behind a sequence's last key the tile holds rows of the next sequence. Their scores are masked, but
+      // P = 0 does not cancel NaN or infinities in V, so the rows that share the last k-step with keys of the
+      // sequence are zeroed, between the tile's landing and its PV products. The wait for the landing lasts as
+      // long as the units before (whose own waits are bounded and end this one), hence its own limit.
+      constexpr uint64_t kTailLimit = 512 * kWaitLimitNs;
+      bool ok = true;
+      int pos = 0, cnt = 0;
+      for (int k = 0; ok; ++k) {
+        const int lin = PAIR ? pair_unit(k) : next_unit(k, true);
+        if (lin < 0) break;
+        const Unit un = unit_at<D, PAIR, VL>(args, lin);
+        pos += 2 * un.n_tiles;  // past the unit: its last V tile is at pos - 1
+        const int cut = un.nkv - (un.n_tiles - 1) * C::BN;
+        if (un.n_tiles == 0 || cut >= C::BN) continue;
+        const uint32_t ph = uint32_t(cnt & 1);
+        ++cnt;
+        ok = __all_sync(0xffffffffu, PAIR ? mbar_wait_cluster(v_land, ph, abort_flag, kTailLimit)
+                                          : mbar_wait(v_land, ph, abort_flag, kTailLimit));
+        if (!ok) break;
+        const int slot = kv_slot(pos - 1);
+        constexpr int UPR = C::ROWB / 16;                 // 16-byte units of a stored row (a chunk of d)
+        constexpr int UNITS = C::V_COLS * C::EB / 16;     // of all chunks
+        const int rows = (C::KSTEP - cut % C::KSTEP) % C::KSTEP;
+        uint8_t* tile = sKV + slot * C::KV_TILE_BYTES;
+        for (int i = lane; i < rows * UNITS; i += 32) {
+          const int r = cut + i / UNITS, u = i % UNITS;  // whole rows, so the swizzle does not matter
+          *reinterpret_cast<uint4*>(tile + (u / UPR) * C::V_CHUNK_BYTES + r * C::ROWB + (u % UPR) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_release_cluster(mapa_shared(v_clean, 0));
+          else
+            mbar_arrive(v_clean);
+        }
+      }
+    }
   } else {
     // ================================ softmax warpgroups ================================
     if (kSplitRegs) regs_inc<C::SM_REGS>();
@@ -676,7 +784,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
     for (int k = 0; ok; ++k) {
       const int lin = PAIR ? pair_unit(k) : next_unit(k, true);
       if (lin < 0) break;
-      const Unit un = unit_at<D, PAIR>(args, lin);
+      const Unit un = unit_at<D, PAIR, VL>(args, lin);
       if (F8) {
         // codes decode as value = code * amax / 448 per (batch, head)
         const int g = un.h / args.group;
@@ -686,10 +794,14 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
         sc_nat = args.scale * dq * dk;
         o_mul = args.amax_v[un.b * args.Hkv + g] / 448.0f;
       }
-      const int q_first = un.q0 + (qt + int(rank)) * C::BM;  // (a pair: NQT = 1, rank 1 takes the second 128 rows)
+      // queries, keys and first row of the sequence (packed sequences: from the unit's first row on, which is
+      // row un.q0 of the packed buffers)
+      const int nq = VL ? un.nq : args.Nq, nkv = VL ? un.nkv : args.Nkv;
+      const int diag = nkv - nq;  // key j visible to query i iff j <= i + diag
+      const int q_first = (VL ? 0 : un.q0) + (qt + int(rank)) * C::BM;  // (a pair: NQT = 1, rank 1 takes the second 128 rows)
       const int q_row = q_first + row;
-      // last key visible to this row (any key index <= lim is visible); rows past Nq are padding
-      const int lim = args.causal ? min(args.Nkv - 1, q_row + diag) : args.Nkv - 1;
+      // last key visible to this row (any key index <= lim is visible); rows past nq are padding
+      const int lim = args.causal ? min(nkv - 1, q_row + diag) : nkv - 1;
       float m_ref = -INFINITY;  // reference max (raw-score units) of the exponentials in l and O
       float l = 0.f;            // running row sum of exp2(c * (s - m_ref))
 
@@ -733,7 +845,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
         const int kbase = j * C::BN;
         // warp-uniform: does any key of this tile fall outside some row's visible range?
         const bool need_mask =
-            (kbase + C::BN > args.Nkv) || (args.causal && kbase + C::BN - 1 > q_first + diag);
+            (kbase + C::BN > nkv) || (args.causal && kbase + C::BN - 1 > q_first + diag);
         if (need_mask) {
 #pragma unroll
           for (int i = 0; i < C::BN; ++i)
@@ -865,9 +977,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
       if (!ok) break;
 
       // ---- epilogue: O = acc / l (once), LSE = scale * m_ref + ln l -------------------------------
-      const bool valid = q_row < args.Nq;
+      const bool valid = q_row < nq;
+      const int out_row = VL ? un.q0 + q_row : q_row;
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(args.o) +
-                            ((size_t(un.b) * args.Nq + (valid ? q_row : 0)) * args.Hq + un.h) * D;
+                            ((size_t(un.b) * args.Nq + (valid ? out_row : 0)) * args.Hq + un.h) * D;
       if (un.n_tiles > 0 && my_tiles == 0) {
         // this tile saw no key: O = 0 (no MMA wrote its accumulator, and no o_final phase was
         // committed for it)
@@ -919,7 +1032,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
         for (int v4 = 0; v4 < D / 8; ++v4) dst[v4] = make_uint4(0, 0, 0, 0);
       }
       if (valid)
-        args.lse[(size_t(un.b) * args.Hq + un.h) * args.Nq + q_row] =
+        args.lse[(size_t(un.b) * args.Hq + un.h) * args.Nq + out_row] =
             (l > 0.f) ? fmaf(m_ref, sc_nat, logf(l)) : -INFINITY;
     }
   }
@@ -937,7 +1050,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
       tmem_dealloc(tmem, C::TMEM_COLS);
   }
   // The last CTA to finish returns the scheduling slot to zero (all CTAs have stopped claiming).
-  if (!PAIR && threadIdx.x == 0) {
+  if (!PAIR && !VL && threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(&g_sched_done[args.sched_slot], 1u) == gridDim.x - 1) {
       atomicExch(&g_sched_next[args.sched_slot], 0u);
@@ -949,6 +1062,25 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
 // ---------------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------------
+// setmaxnreg.inc waits until the registers it asks for are free in the CTA's launch allocation,
+// so a split whose total exceeds that allocation would never proceed: refuse to launch it.
+template <int D, bool F8, bool PAIR, bool VL>
+static attn_status_t fwd_regs_fit() {
+  using C = FwdCfg<D, F8, PAIR>;
+  if (!C::SPLIT_REGS) return ATTN_OK;
+  static std::atomic<int> regs_ok{0};  // 0 unknown, 1 fits, 2 does not (same binary on every device)
+  int st = regs_ok.load(std::memory_order_relaxed);
+  if (st == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, attn_fwd_kernel<D, F8, PAIR, VL>) != cudaSuccess) return ATTN_ERR_CUDA;
+    const long long pool = (long long)fa.numRegs * C::THREADS;
+    const long long need = 128LL * C::CTRL_REGS + 128LL * C::NSMWG * C::SM_REGS;
+    st = pool >= need ? 1 : 2;
+    regs_ok.store(st, std::memory_order_relaxed);
+  }
+  return st == 1 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
 // F8: q and k are e4m3 codes [B, N, H, d], v is the transposed code tensor [B, Hkv, d, Nkv] and
 // amax_* the per-(batch, head) dequantization maxima; otherwise bf16 tensors and null amax.
 template <int D, bool F8, bool PAIR = false>
@@ -956,7 +1088,7 @@ static attn_status_t launch_fwd(const void* q, const void* k, const void* v, voi
                                 int Hkv, int Nq, int Nkv, float scale, int causal, const float* amax_q,
                                 const float* amax_k, const float* amax_v, cudaStream_t stream) {
   using C = FwdCfg<D, F8, PAIR>;
-  auto kernel = attn_fwd_kernel<D, F8, PAIR>;
+  auto kernel = attn_fwd_kernel<D, F8, PAIR, false>;
   CUtensorMap tmQ, tmK, tmV;
   const uint32_t swz = C::ROWB == 128 ? 128u : 64u;
   if (F8) {
@@ -973,22 +1105,9 @@ static attn_status_t launch_fwd(const void* q, const void* k, const void* v, voi
 
   if (ensure_dyn_smem(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  // setmaxnreg.inc waits until the registers it asks for are free in the CTA's launch allocation,
-  // so a split whose total exceeds that allocation would never proceed: refuse to launch it.
-  if (C::SPLIT_REGS) {
-    static std::atomic<int> regs_ok{0};  // 0 unknown, 1 fits, 2 does not (same binary on every device)
-    int st = regs_ok.load(std::memory_order_relaxed);
-    if (st == 0) {
-      cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return ATTN_ERR_CUDA;
-      const long long pool = (long long)fa.numRegs * C::THREADS;
-      const long long need = 128LL * C::CTRL_REGS + 128LL * C::NSMWG * C::SM_REGS;
-      st = pool >= need ? 1 : 2;
-      regs_ok.store(st, std::memory_order_relaxed);
-    }
-    if (st != 1) return ATTN_ERR_UNSUPPORTED;
-  }
-  FwdArgs a;
+  const attn_status_t regs = fwd_regs_fit<D, F8, PAIR, false>();
+  if (regs != ATTN_OK) return regs;
+  FwdArgs a = {};
   a.o = o;
   a.lse = lse;
   a.B = B;
@@ -1052,6 +1171,79 @@ static attn_status_t launch_fwd(const void* q, const void* k, const void* v, voi
   a.sched_slot = int(g_fwd_launch_count.fetch_add(1) % kSchedSlots);
   kernel<<<dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, stream>>>(tmQ, tmK, tmV, a);
   return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : (cudaGetLastError(), ATTN_ERR_CUDA);
+}
+
+// Packed sequences: the plan (`plan`, made by an earlier kernel of the stream) names the units; the launch is
+// programmatic, so that set-up overlaps the plan kernel. max_blocks bounds the planned blocks.
+template <int D, bool PAIR>
+static attn_status_t launch_fwd_varlen(const VarPlan& plan, const void* q, const void* k, const void* v, void* o,
+                                       float* lse, int Tq, int Tk, int Hq, int Hkv, long long qs, long long ks,
+                                       long long vs, float scale, int causal, cudaStream_t stream) {
+  using C = FwdCfg<D, false, PAIR>;
+  auto kernel = attn_fwd_kernel<D, false, PAIR, true>;
+  CUtensorMap tmQ, tmK, tmV;
+  const uint32_t swz = C::ROWB == 128 ? 128u : 64u;
+  if (!encode_tile_map(&tmQ, q, D, Hq, Tq, 1, C::CHUNK, C::BM, swz, qs) ||
+      !encode_tile_map(&tmK, k, D, Hkv, Tk, 1, C::CHUNK, C::K_ROWS, swz, ks) ||
+      !encode_tile_map(&tmV, v, D, Hkv, Tk, 1, C::CHUNK, C::BN, swz, vs))
+    return ATTN_ERR_CUDA;
+  if (ensure_dyn_smem(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES) != cudaSuccess) return ATTN_ERR_CUDA;
+  const attn_status_t regs = fwd_regs_fit<D, false, PAIR, true>();
+  if (regs != ATTN_OK) return regs;
+  FwdArgs a = {};
+  a.o = o;
+  a.lse = lse;
+  a.B = 1;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.Nq = Tq;
+  a.Nkv = Tk;
+  a.group = Hq / Hkv;
+  a.causal = causal;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.timeout_ns = kWaitLimitNs;
+  a.var_units = plan.units;
+  a.var_count = plan.count;
+  a.var_claim = plan.claim;
+  const long long units = plan.max_blocks * Hq;
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  long long ctas = units < sms ? units : sms;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (PAIR) {
+    const int pairs = max_pairs(reinterpret_cast<const void*>(kernel), C::THREADS, C::SMEM_BYTES);
+    if (pairs <= 0) return ATTN_ERR_CUDA;
+    ctas = 2 * (units < pairs ? units : pairs);
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    lc.numAttrs = 2;
+  }
+  lc.gridDim = dim3(unsigned(ctas));
+  lc.blockDim = dim3(C::THREADS);
+  lc.dynamicSmemBytes = C::SMEM_BYTES;
+  lc.stream = stream;
+  if (cudaLaunchKernelEx(&lc, kernel, tmQ, tmK, tmV, a) != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
+  return ATTN_OK;
+}
+
+attn_status_t fwd_varlen_dispatch(const VarPlan& plan, const void* q, const void* k, const void* v, void* o,
+                                  float* lse, int Tq, int Tk, int Hq, int Hkv, int d, long long qs, long long ks,
+                                  long long vs, float scale, int causal, cudaStream_t stream) {
+  switch (d) {
+    case 32: return launch_fwd_varlen<32, false>(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, qs, ks, vs, scale, causal, stream);
+    case 64: return launch_fwd_varlen<64, false>(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, qs, ks, vs, scale, causal, stream);
+    case 128: return launch_fwd_varlen<128, false>(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, qs, ks, vs, scale, causal, stream);
+    case 256: return launch_fwd_varlen<256, true>(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, qs, ks, vs, scale, causal, stream);
+    default: return ATTN_ERR_UNSUPPORTED;
+  }
 }
 
 attn_status_t fwd_dispatch(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,

@@ -20,6 +20,14 @@ enum : unsigned int {
 // 8k x 8k head takes well under a millisecond), so reaching it means the pipeline is broken.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
+// Packed sequences: one block of query rows of one sequence, as the plan kernel lists them.
+struct __align__(16) VarUnit {
+  int q_row;  // packed row of the block's first query
+  int nq;     // the sequence's queries from that row on
+  int k_row;  // packed row of the sequence's first key
+  int nkv;    // its keys
+};
+
 struct FwdArgs {
   void* o;
   float* lse;
@@ -35,6 +43,10 @@ struct FwdArgs {
   const float* amax_q;  // 8-bit path: per-(batch, head) maxima the codes were scaled by; else null
   const float* amax_k;
   const float* amax_v;
+  // packed sequences (B = 1, Nq and Nkv are the rows of the buffers): the plan in the call's workspace
+  const VarUnit* var_units;
+  const int* var_count;        // blocks of query rows listed
+  unsigned int* var_claim;     // next unit (block x query head)
 };
 
 bool is_aligned16(const void* p);
@@ -57,12 +69,13 @@ int max_pairs(const void* func, int threads, int smem_bytes);
 // (none). Maps are cached per (pointer, shape, box, swizzle): a map holds only the address and the
 // geometry, so a cached copy is valid wherever the same key comes back. Returns false on failure.
 bool encode_tile_map(CUtensorMap* map, const void* base, int d, int heads, int rows, int outer, int box_cols,
-                     int box_rows, unsigned swizzle_bytes);
+                     int box_rows, unsigned swizzle_bytes, long long row_stride = 0);
 
 // The general form: a 4-d tensor of elem_bytes-sized elements (1: 8-bit codes, 2: bf16, 4: fp32) with dense
 // strides, dims[0] innermost, box[] elements per dimension; cached like encode_tile_map.
+// row_stride, if not 0: elements between consecutive indices of dims[2] (a token stride).
 bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long long* dims, const int* box,
-                unsigned swizzle_bytes);
+                unsigned swizzle_bytes, long long row_stride = 0);
 
 // Opts `func` into `bytes` of dynamic shared memory on the current device. The attribute belongs to
 // the function on one device, so it is set once per (function, device) and again only when a
@@ -81,6 +94,17 @@ attn_status_t fwd_dispatch(const void* q, const void* k, const void* v, void* o,
 attn_status_t fwd_fp8_dispatch(const void* q8, const void* k8, const void* vt8, const float* amax_q,
                                const float* amax_k, const float* amax_v, void* o, float* lse, int B, int Hq, int Hkv,
                                int Nq, int Nkv, int d, float scale, int causal, cudaStream_t stream);
+
+// The plan of a packed call, in its workspace (attn_varlen.cu).
+struct VarPlan {
+  VarUnit* units;        // [max_blocks]
+  int* count;            // blocks listed
+  unsigned int* claim;   // 0 when the plan is made
+  long long max_blocks;
+};
+attn_status_t fwd_varlen_dispatch(const VarPlan& plan, const void* q, const void* k, const void* v, void* o,
+                                  float* lse, int Tq, int Tk, int Hq, int Hkv, int d, long long qs, long long ks,
+                                  long long vs, float scale, int causal, cudaStream_t stream);
 
 attn_status_t fp8_quantize_dispatch(const void* x, const float* signs, void* codes, float* amax, int B, int N, int H,
                                     int transpose, cudaStream_t stream);

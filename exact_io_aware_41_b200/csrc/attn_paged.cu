@@ -109,11 +109,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
   return d;
 }
 
-// Programmatic dependent launch: the next kernel of the stream may start its preamble, and waits here until
-// this one's results are in memory.
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Byte address of element (row, col) of a tile written by TMA: 128-byte swizzled chunks of 64 columns, or
 // plain 64-byte rows at d = 32.
 template <int D>
