@@ -69,8 +69,8 @@ constexpr int OFF_Q0 = 3 * TILE_BYTES;        // stage s: Q at OFF_Q0 + 2s tiles
 constexpr int OFF_LSE0 = 7 * TILE_BYTES;      // stage s: LSE' at OFF_LSE0 + s * 1024, D 512 bytes later
 constexpr int OFF_BAR = OFF_LSE0 + 2 * 1024;
 // kv_full, q_full[2], q_empty[2], s_full, p_full, dq_full, dq_free, dkv_full, dk_done[2], epi_full, epi_free,
-// st_full, pt_full
-constexpr int NBARS = 16;
+// st_full, pt_full, t_land, t_clean
+constexpr int NBARS = 18;
 constexpr int SMEM_BYTES = OFF_BAR + NBARS * 8 + 16;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 }  // namespace bwd
@@ -86,7 +86,19 @@ struct BwdArgs {
   float scale_log2;
   float scale;
   unsigned long long timeout_ns;
+  // packed sequences (B = 1, Nq and Nkv are the rows of the buffers, Nq_pad the length of a head's LSE' and D
+  // rows): the planned key blocks, in the call's workspace
+  const VarUnit* var_units;
+  const int* var_count;
 };
+
+// Packed sequences: where a sequence's rows start in the padded arrays of the workspace. Every sequence starts at
+// a multiple of `unit` rows, so that whole tiles (LSE', D) and whole boxes (the dQ accumulator) belong to one
+// sequence; (T / unit + S) * unit rows hold them all.
+__host__ __device__ __forceinline__ size_t padded_row(int first_row, int seq, int unit) {
+  return (size_t(first_row / unit) + seq) * unit;
+}
+constexpr int kAccRows = 32;  // rows of a dQ box
 
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -118,12 +130,17 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void*
 
 // First query tile whose rows see some key of block kb (causal: key j visible to row i iff
 // j <= i + Nkv - Nq).
-__device__ __forceinline__ int first_q_tile(const BwdArgs& a, int kb) {
-  if (!a.causal) return 0;
-  const int lo = kb * bwd::BN - (a.Nkv - a.Nq);  // smallest row that sees key kb * BN
+// Keys count from the block's first one here, of which `nkv` are left; `nq` queries.
+__device__ __forceinline__ int first_q_tile(int causal, int nq, int nkv) {
+  if (!causal) return 0;
+  const int lo = nq - nkv;  // smallest row that sees the block's first key
   return lo <= 0 ? 0 : lo / bwd::BM;
 }
 
+// VL: packed sequences. A key block, and the query tiles it walks, belong to one sequence; tiles that reach past
+// its end hold rows of the next sequence, which are masked where they are rows or columns of a product, and
+// zeroed (or left out, by whole k-steps) where a product sums over them.
+template <bool VL>
 __global__ void __launch_bounds__(bwd::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -150,18 +167,38 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
   uint64_t* epi_free = bars + 13; // one phase per dK / dV tile: the TMA unit has read it
   uint64_t* st_full = bars + 14;  // one phase per step: S^T is in (s_full: dP^T too)
   uint64_t* pt_full = bars + 15;  // one phase per step: P^T is in (p_full: dS^T too)
+  // packed sequences, one phase per tile cut off by its sequence's end (the K tile, then the steps' Q and dO):
+  // it has landed (the MMA thread saw it) / its tail rows are zero
+  uint64_t* t_land = bars + 16;
+  uint64_t* t_clean = bars + 17;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t T = args.timeout_ns;
-  // unit: key block kb (heaviest first), batch b, kv head g
+  // unit: key block (heaviest first), batch b, kv head g; its first key's row, the keys from there on, the first
+  // row and the number of the queries, where those start in the LSE' / D rows and in the dQ accumulator
   const int per_kb = args.B * args.Hkv;
   const int kb = blockIdx.x / per_kb;
-  const int b = (blockIdx.x % per_kb) / args.Hkv;
+  const int b = VL ? 0 : (blockIdx.x % per_kb) / args.Hkv;
   const int g = blockIdx.x % args.Hkv;
-  const int n_qt = (args.Nq + BM - 1) / BM;
-  const int qt0 = first_q_tile(args, kb);
+  int k_row = kb * BN, nkv = args.Nkv - kb * BN, q_row = 0, nq = args.Nq, acc_row = 0;
+  size_t lse_row = 0;
+  if constexpr (VL) {
+    pdl_wait();  // the pre-pass, with the plan, is in memory
+    pdl_launch();
+    if (kb >= *args.var_count) return;  // (the grid is sized by a bound)
+    const VarUnit u = args.var_units[kb];
+    k_row = u.k_row;
+    nkv = u.nkv;
+    q_row = u.q_row;
+    nq = u.nq;
+    lse_row = padded_row(q_row, u.seq, BM);
+    acc_row = int(padded_row(q_row, u.seq, kAccRows));
+  }
+  const int diag = nkv - nq;  // the block's key j is visible to query i iff j <= i + diag
+  const int n_qt = (nq + BM - 1) / BM;
+  const int qt0 = first_q_tile(args.causal, nq, nkv);
   const int steps_per_head = qt0 < n_qt ? n_qt - qt0 : 0;
   const int n_steps = steps_per_head * args.group;
 
@@ -182,6 +219,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     mbar_init(&dk_done[1], 1);
     mbar_init(epi_full, NSW);  // one arrival per elementwise warp
     mbar_init(epi_free, 1);
+    mbar_init(t_land, 1);
+    mbar_init(t_clean, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -209,8 +248,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       prefetch_tensormap(&tmDO);
       mbar_arrive_expect_tx(kv_full, 2 * TILE_BYTES);
       for (int c = 0; c < 2; ++c) {
-        tma_load_4d(smem + OFF_K + c * CHUNK_BYTES, &tmK, kv_full, c * 64, g, kb * BN, b);
-        tma_load_4d(smem + OFF_V + c * CHUNK_BYTES, &tmV, kv_full, c * 64, g, kb * BN, b);
+        tma_load_4d(smem + OFF_K + c * CHUNK_BYTES, &tmK, kv_full, c * 64, g, k_row, b);
+        tma_load_4d(smem + OFF_V + c * CHUNK_BYTES, &tmV, kv_full, c * 64, g, k_row, b);
       }
       int t = 0;
       for (; t < n_steps; ++t) {
@@ -222,10 +261,10 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         uint8_t* sq = smem + OFF_Q0 + 2 * st * TILE_BYTES;
         mbar_arrive_expect_tx(&q_full[st], 2 * TILE_BYTES + 2 * BM * 4);
         for (int c = 0; c < 2; ++c) {
-          tma_load_4d(sq + c * CHUNK_BYTES, &tmQ, &q_full[st], c * 64, h, qt * BM, b);
-          tma_load_4d(sq + TILE_BYTES + c * CHUNK_BYTES, &tmDO, &q_full[st], c * 64, h, qt * BM, b);
+          tma_load_4d(sq + c * CHUNK_BYTES, &tmQ, &q_full[st], c * 64, h, q_row + qt * BM, b);
+          tma_load_4d(sq + TILE_BYTES + c * CHUNK_BYTES, &tmDO, &q_full[st], c * 64, h, q_row + qt * BM, b);
         }
-        const size_t row = size_t(b * args.Hq + h) * args.Nq_pad + size_t(qt) * BM;
+        const size_t row = size_t(b * args.Hq + h) * args.Nq_pad + lse_row + size_t(qt) * BM;
         bulk_load(smem + OFF_LSE0 + st * 1024, args.lse2 + row, BM * 4, &q_full[st]);
         bulk_load(smem + OFF_LSE0 + st * 1024 + 512, args.dd + row, BM * 4, &q_full[st]);
       }
@@ -248,8 +287,17 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       constexpr uint32_t idesc_tmn = idesc_bf16_f32(128, 128, 0, 1);   // A from TMEM, B MN-major
       constexpr uint32_t idesc_mnmn = idesc_bf16_f32(128, 128, 1, 1);  // A, B MN-major
       bool ok = mbar_wait(kv_full, 0, abort_flag, T);
+      int tails = 0;  // tiles given to the tail warp (phase of t_clean)
+      const int keys = VL ? min(nkv, BN) : BN;
+      if (VL && ok && keys < BN) {
+        mbar_arrive(t_land);
+        ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
+      }
       for (int t = 0; t < n_steps && ok; ++t) {
         const int st = t & 1;
+        int h, qt;
+        step_coords(t, h, qt);
+        const int queries = VL ? min(nq - qt * BM, BM) : BM;  // of this step's tile
         const uint32_t sq = smem_u32(smem + OFF_Q0 + 2 * st * TILE_BYTES);
         const uint64_t dQ_k = smem_desc(sq, 16, 1024, kLayoutSW128);
         const uint64_t dDO_k = smem_desc(sq + TILE_BYTES, 16, 1024, kLayoutSW128);
@@ -257,6 +305,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         const uint64_t dDO_mn = smem_desc(sq + TILE_BYTES, CHUNK_BYTES, 1024, kLayoutSW128);
         ok = mbar_wait(&q_full[st], uint32_t((t >> 1) & 1), abort_flag, T);
         if (!ok) break;
+        if (VL && queries < BM) mbar_arrive(t_land);
         tc_fence_after();
         // S^T = K Q^T into [0, 128), once the previous step's dQ (there) has been read out
         if (t > 0) {
@@ -284,24 +333,31 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         // A = P^T / dS^T: queries 16kk .. 16kk+15 are columns 8 (kk % 2) .. of chunk kk / 2, which
         // starts at column 32 (kk / 2)
         ok = mbar_wait(pt_full, uint32_t(t & 1), abort_flag, T);
+        if (VL && ok && queries < BM) ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < BM / 16; ++kk)
+        for (int kk = 0; kk < BM / 16; ++kk) {
+          if (VL && kk * 16 >= queries) break;
           umma_ts(tmem + DV_COL, tmem + S_COL + 32 * (kk / 2) + 8 * (kk % 2),
                   dDO_mn + uint64_t((kk * 16 * 128) >> 4), idesc_tmn, (t > 0 || kk > 0) ? 1u : 0u);
+        }
         ok = mbar_wait(p_full, uint32_t(t & 1), abort_flag, T);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          if (VL && kk * 16 >= keys) break;
           umma_ss(tmem + S_COL, dDS_mn + uint64_t((kk * 16 * 128) >> 4), dK_mn + uint64_t((kk * 16 * 128) >> 4),
                   idesc_mnmn, kk > 0 ? 1u : 0u);
+        }
         umma_commit(dq_full);
 #pragma unroll
-        for (int kk = 0; kk < BM / 16; ++kk)
+        for (int kk = 0; kk < BM / 16; ++kk) {
+          if (VL && kk * 16 >= queries) break;
           umma_ts(tmem + DK_COL, tmem + DP_COL + 32 * (kk / 2) + 8 * (kk % 2),
                   dQ_mn + uint64_t((kk * 16 * 128) >> 4), idesc_tmn, (t > 0 || kk > 0) ? 1u : 0u);
+        }
         umma_commit(&dk_done[t & 1]);
         if (t == n_steps - 1) umma_commit(dkv_full);
       }
@@ -315,6 +371,33 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     __syncwarp();
   } else if (warp < 4) {
     regs_dec<CTRL_REGS>();
+    if (VL && warp == 3) {
+      // ================================ tail rows ================================
+      // dV, dK sum over the queries of a tile and dQ over its keys: P = dS = 0 does not cancel NaN or infinities in
+      // rows of the next sequence, so those that share the last k-step with the sequence's rows are zeroed once
+      // the tile has landed, while the elementwise warps work. The phases of t_land may lie many steps apart,
+      // whose own waits are bounded and end this one, hence its own limit.
+      constexpr uint64_t kTailLimit = 512 * kWaitLimitNs;
+      int tails = 0;
+      // zeroes rows [cut, next multiple of 16) of n tiles at `tile`, once the next phase of t_land is there
+      auto clean = [&](uint8_t* tile, int n, int cut) -> bool {
+        if (!__all_sync(0xffffffffu, mbar_wait(t_land, uint32_t(tails++ & 1), abort_flag, kTailLimit))) return false;
+        const int rows = (16 - cut % 16) % 16;
+        for (int i = lane; i < n * rows * 16; i += 32) {
+          const int r = cut + (i / 16) % rows, u = i % 16, which = i / 16 / rows;  // whole rows: swizzled or not
+          *reinterpret_cast<uint4*>(tile + which * TILE_BYTES + (u / 8) * CHUNK_BYTES + r * 128 + (u % 8) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(t_clean);
+        return true;
+      };
+      bool ok = n_steps == 0 || nkv >= BN || clean(smem + OFF_K, 1, nkv);
+      if (n_steps > 0 && nq % BM != 0)
+        for (int t = steps_per_head - 1; t < n_steps && ok; t += steps_per_head)  // every head's last tile
+          ok = clean(smem + OFF_Q0 + 2 * (t & 1) * TILE_BYTES, 2, nq % BM);
+    }
   } else if (warp >= 4 + NSW) {
     // ================================ dQ warps ================================
     // Per step, thread = query row q0 + row: once the dQ product is done, read it from TMEM (columns
@@ -358,9 +441,9 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && row0 < args.Nq) {  // rows past Nq are clipped by the TMA unit
-        tma_reduce_add_4d(&tmDQ, buf + 2 * 16384, 64, h, row0, b);
-        tma_reduce_add_4d(&tmDQ, buf + 3 * 16384, 96, h, row0, b);
+      if (lane == 0 && row0 < nq) {  // rows past Nq are clipped by the TMA unit (packed: land in padding rows)
+        tma_reduce_add_4d(&tmDQ, buf + 2 * 16384, 64, h, acc_row + row0, b);
+        tma_reduce_add_4d(&tmDQ, buf + 3 * 16384, 96, h, acc_row + row0, b);
       }
       uint32_t o[2][32];
       tmem_ld32(lane_addr + S_COL, o[0]);
@@ -380,9 +463,9 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (row0 < args.Nq) {
-          tma_reduce_add_4d(&tmDQ, buf, 0, h, row0, b);
-          tma_reduce_add_4d(&tmDQ, buf + 16384, 32, h, row0, b);
+        if (row0 < nq) {
+          tma_reduce_add_4d(&tmDQ, buf, 0, h, acc_row + row0, b);
+          tma_reduce_add_4d(&tmDQ, buf + 16384, 32, h, acc_row + row0, b);
         }
         bulk_commit_group();
         bulk_wait_group_read0();  // the TMA unit has read the boxes: the buffer may be refilled
@@ -404,9 +487,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     const int row = wq * 32 + lane;   // TMEM lane: key row (softmax, dK dV) or query row (dQ)
     const uint32_t lane_addr = tmem + (uint32_t(wq * 32) << 16);
     const float c = args.scale_log2;
-    const int key = kb * BN + row;
-    const bool key_ok = key < args.Nkv;
-    const int diag = args.Nkv - args.Nq;
+    const int key = row;  // from the block's first key
+    const bool key_ok = key < nkv;
     auto wait_warp = [&](uint64_t* bar, uint32_t ph) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag, T));
     };
@@ -434,7 +516,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         // warp-uniform: does some (key, query) of this 32 x 32 block fall outside the mask? (rows
         // past Nq need no test: their LSE' is +inf, so P = 0)
         const int qf = q0 + cc * 32;
-        const bool need_mask = (kb * BN + BN > args.Nkv) || (args.causal && kb * BN + BN - 1 > qf + diag);
+        const bool need_mask = BN > nkv || (VL && qf + 32 > nq) || (args.causal && BN - 1 > qf + diag);
         uint32_t pk[16];
 #pragma unroll
         for (int i4 = 0; i4 < 8; ++i4) {
@@ -448,8 +530,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
                                    make_float2(c, c), make_float2(-lv[u], -lv[u + 1]));
             float2 p = make_float2(ex2(x.x), ex2(x.y));
             if (need_mask) {
-              if (!(key_ok && (!args.causal || key <= q0 + qi + diag))) p.x = 0.f;
-              if (!(key_ok && (!args.causal || key <= q0 + qi + 1 + diag))) p.y = 0.f;
+              if (!(key_ok && (!args.causal || key <= q0 + qi + diag) && (!VL || q0 + qi < nq))) p.x = 0.f;
+              if (!(key_ok && (!args.causal || key <= q0 + qi + 1 + diag) && (!VL || q0 + qi + 1 < nq))) p.y = 0.f;
             }
             pf[cx][4 * i4 + u] = p.x;
             pf[cx][4 * i4 + u + 1] = p.y;
@@ -479,6 +561,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         tmem_ld_wait();
         tmem_reg_fence32(dpv);
         uint32_t dk2[16];
+        // packed: keys and queries of other sequences, where dP may be anything (P = 0 there)
+        const bool foreign = VL && (BN > nkv || q0 + cc * 32 + 32 > nq);
 #pragma unroll
         for (int i4 = 0; i4 < 8; ++i4) {
           const float4 d4 = *reinterpret_cast<const float4*>(s_dd + cc * 32 + 4 * i4);
@@ -486,9 +570,14 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const int u = 2 * h2;
-            const float2 ds = fmul2(make_float2(pf[cx][4 * i4 + u], pf[cx][4 * i4 + u + 1]),
-                                    fadd2(make_float2(__uint_as_float(dpv[4 * i4 + u]), __uint_as_float(dpv[4 * i4 + u + 1])),
-                                          make_float2(-dv4[u], -dv4[u + 1])));
+            float2 ds = fmul2(make_float2(pf[cx][4 * i4 + u], pf[cx][4 * i4 + u + 1]),
+                              fadd2(make_float2(__uint_as_float(dpv[4 * i4 + u]), __uint_as_float(dpv[4 * i4 + u + 1])),
+                                    make_float2(-dv4[u], -dv4[u + 1])));
+            if (foreign) {
+              const int qi = q0 + cc * 32 + 4 * i4 + u;
+              if (!key_ok || qi >= nq) ds.x = 0.f;
+              if (!key_ok || qi + 1 >= nq) ds.y = 0.f;
+            }
             dk2[2 * i4 + h2] = pack_bf16x2(ds.x, ds.y);
           }
         }
@@ -517,7 +606,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     if (key_ok && n_steps == 0) {
       for (int which = 0; which < 2; ++which) {
         uint4* dz = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(which ? args.dv : args.dk) +
-                                             ((size_t(b) * args.Nkv + key) * args.Hkv + g) * D + 32 * CPW * cw);
+                                             ((size_t(b) * args.Nkv + k_row + key) * args.Hkv + g) * D + 32 * CPW * cw);
         for (int v4 = 0; v4 < 4 * CPW; ++v4) dz[v4] = make_uint4(0, 0, 0, 0);
       }
     }
@@ -539,6 +628,17 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             pk[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
+          if (VL && nkv < BN) {
+            // the block's other rows belong to the next sequence: row by row, without the TMA unit
+            if (key_ok) {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(which ? args.dv : args.dk) +
+                                                    (size_t(k_row + key) * args.Hkv + g) * D + (CPW * cw + cx) * 32);
+#pragma unroll
+              for (int v4 = 0; v4 < 4; ++v4)
+                dst[v4] = make_uint4(pk[4 * v4], pk[4 * v4 + 1], pk[4 * v4 + 2], pk[4 * v4 + 3]);
+            }
+            continue;
+          }
 #pragma unroll
           for (int v4 = 0; v4 < 4; ++v4) {
             const int unit = cx * 4 + v4;  // 16-byte unit of the row's 128 bytes
@@ -548,6 +648,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
                          : "memory");
           }
         }
+        if (VL && nkv < BN) continue;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(epi_full);
@@ -555,8 +656,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
           // every warp's rows are in: store the tile, and free it once the TMA unit has read it
           if (mbar_wait(epi_full, uint32_t(which), abort_flag, T)) {
             const CUtensorMap* m = which == 0 ? &tmDK : &tmDV;
-            tma_store_4d(m, smem + OFF_DS, 0, g, kb * BN, b);
-            tma_store_4d(m, smem + OFF_DS + CHUNK_BYTES, 64, g, kb * BN, b);
+            tma_store_4d(m, smem + OFF_DS, 0, g, k_row, b);
+            tma_store_4d(m, smem + OFF_DS + CHUNK_BYTES, 64, g, k_row, b);
             bulk_commit_group();
             bulk_wait_group_read0();
             mbar_arrive(epi_free);
@@ -639,6 +740,26 @@ __global__ void attn_bwd_post_kernel(const float* __restrict__ acc, __nv_bfloat1
   }
 }
 
+// Opts the kernel into its shared memory and checks its register split: setmaxnreg.inc waits until the
+// registers it asks for are free in the CTA's launch allocation, so a split whose total exceeds that
+// allocation would never proceed: refuse to launch it.
+template <bool VL>
+static attn_status_t bwd_ready() {
+  using namespace bwd;
+  if (ensure_dyn_smem(reinterpret_cast<const void*>(attn_bwd_kernel<VL>), SMEM_BYTES) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  static std::atomic<int> regs_ok{0};  // 0 unknown, 1 fits, 2 does not (same binary on every device)
+  int st = regs_ok.load(std::memory_order_relaxed);
+  if (st == 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, attn_bwd_kernel<VL>) != cudaSuccess) return ATTN_ERR_CUDA;
+    const long long need = 128LL * (CTRL_REGS + 2 * EW_REGS + DQ_REGS);
+    st = (long long)fa.numRegs * THREADS >= need ? 1 : 2;
+    regs_ok.store(st, std::memory_order_relaxed);
+  }
+  return st == 1 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
 size_t bwd_workspace(int B, int Hq, int Nq, int d) {
   const size_t nq_pad = (size_t(Nq) + 127) / 128 * 128;
   const size_t acc = size_t(B) * Nq * Hq * d * sizeof(float);
@@ -669,21 +790,8 @@ attn_status_t bwd_dispatch(const void* q, const void* k, const void* v, const vo
     const int box[4] = {32, 1, 32, 1};
     if (!encode_map(&tmDQ, acc, 4, dims, box, 128)) return ATTN_ERR_CUDA;
   }
-  if (ensure_dyn_smem(reinterpret_cast<const void*>(attn_bwd_kernel), SMEM_BYTES) != cudaSuccess) return ATTN_ERR_CUDA;
-  {
-    // setmaxnreg.inc waits until the registers it asks for are free in the CTA's launch allocation,
-    // so a split whose total exceeds that allocation would never proceed: refuse to launch it
-    static std::atomic<int> regs_ok{0};  // 0 unknown, 1 fits, 2 does not (same binary on every device)
-    int st = regs_ok.load(std::memory_order_relaxed);
-    if (st == 0) {
-      cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, attn_bwd_kernel) != cudaSuccess) return ATTN_ERR_CUDA;
-      const long long need = 128LL * (CTRL_REGS + 2 * EW_REGS + DQ_REGS);
-      st = (long long)fa.numRegs * THREADS >= need ? 1 : 2;
-      regs_ok.store(st, std::memory_order_relaxed);
-    }
-    if (st != 1) return ATTN_ERR_UNSUPPORTED;
-  }
+  const attn_status_t ready = bwd_ready<false>();
+  if (ready != ATTN_OK) return ready;
   {
     // the row pass: rows are 16-lane groups, two per warp; about 16 warps per SM in flight
     const long long rows = (long long)B * Nq * Hq;
@@ -695,7 +803,7 @@ attn_status_t bwd_dispatch(const void* q, const void* k, const void* v, const vo
         reinterpret_cast<const __nv_bfloat16*>(o), reinterpret_cast<const __nv_bfloat16*>(dout), lse, lse2, dd, acc, B,
         Nq, Hq, Nq_pad);
   }
-  BwdArgs a;
+  BwdArgs a = {};
   a.dk = dk;
   a.dv = dv;
   a.dq_acc = acc;
@@ -715,11 +823,62 @@ attn_status_t bwd_dispatch(const void* q, const void* k, const void* v, const vo
   a.timeout_ns = kWaitLimitNs;
   const long long grid = (long long)a.n_kb * B * Hkv;
   if (grid > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
-  attn_bwd_kernel<<<dim3(unsigned(grid)), THREADS, SMEM_BYTES, stream>>>(tmQ, tmK, tmV, tmDO, tmDQ, tmDK, tmDV, a);
+  attn_bwd_kernel<false><<<dim3(unsigned(grid)), THREADS, SMEM_BYTES, stream>>>(tmQ, tmK, tmV, tmDO, tmDQ, tmDK, tmDV, a);
   const size_t n4 = size_t(B) * Nq * Hq * D / 4;
   attn_bwd_post_kernel<<<dim3(unsigned(n4 / 256 + 1 < 8192 ? n4 / 256 + 1 : 8192)), 256, 0, stream>>>(
       acc, reinterpret_cast<__nv_bfloat16*>(dq), n4, scale);
   return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : (cudaGetLastError(), ATTN_ERR_CUDA);
+}
+
+// Packed sequences: the pre-pass (with the plan) is an earlier kernel of the stream; see attn_varlen.cu for the
+// workspace. dims of the padded arrays: acc_rows rows of Hq x 128 fp32, lse_rows per head.
+attn_status_t bwd_varlen_launch(const VarPlan& plan, const void* q, const void* k, const void* v, const void* dout,
+                                void* dk, void* dv, float* acc, long long acc_rows, const float* lse2, const float* dd,
+                                long long lse_rows, int Tq, int Tk, int Hq, int Hkv, long long qs, long long ks,
+                                long long vs, float scale, int causal, cudaStream_t stream) {
+  using namespace bwd;
+  CUtensorMap tmQ, tmK, tmV, tmDO, tmDK, tmDV, tmDQ;
+  const long long dims[4] = {D, Hq, acc_rows, 1};
+  const int box[4] = {32, 1, kAccRows, 1};
+  if (!encode_tile_map(&tmQ, q, D, Hq, Tq, 1, 64, BM, 128, qs) || !encode_tile_map(&tmK, k, D, Hkv, Tk, 1, 64, BN, 128, ks) ||
+      !encode_tile_map(&tmV, v, D, Hkv, Tk, 1, 64, BN, 128, vs) || !encode_tile_map(&tmDO, dout, D, Hq, Tq, 1, 64, BM, 128) ||
+      !encode_tile_map(&tmDK, dk, D, Hkv, Tk, 1, 64, BN, 128) || !encode_tile_map(&tmDV, dv, D, Hkv, Tk, 1, 64, BN, 128) ||
+      !encode_map(&tmDQ, acc, 4, dims, box, 128))
+    return ATTN_ERR_CUDA;
+  const attn_status_t ready = bwd_ready<true>();
+  if (ready != ATTN_OK) return ready;
+  BwdArgs a = {};
+  a.dk = dk;
+  a.dv = dv;
+  a.dq_acc = acc;
+  a.lse2 = lse2;
+  a.dd = dd;
+  a.B = 1;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.Nq = Tq;
+  a.Nkv = Tk;
+  a.Nq_pad = int(lse_rows);
+  a.group = Hq / Hkv;
+  a.causal = causal;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale = scale;
+  a.timeout_ns = kWaitLimitNs;
+  a.var_units = plan.units;
+  a.var_count = plan.count;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(unsigned(plan.max_blocks * Hkv));
+  lc.blockDim = dim3(THREADS);
+  lc.dynamicSmemBytes = SMEM_BYTES;
+  lc.stream = stream;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, attn_bwd_kernel<true>, tmQ, tmK, tmV, tmDO, tmDQ, tmDK, tmDV, a) != cudaSuccess)
+    return cudaGetLastError(), ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 }  // namespace attn

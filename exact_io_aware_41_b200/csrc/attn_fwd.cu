@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   const uint32_t tmem = *tmem_holder;
   if constexpr (VL) {
     pdl_wait();  // the plan, a kernel of its own, is in memory
-    total_units = *args.var_count * args.Hq;
+    total_units = max(0, *args.var_count) * args.Hq;
   }
   // With two softmax warpgroups the 128 control threads give registers to the 256 softmax threads:
   // 128 * 104 + 256 * 192 = 62464 <= 384 * 168 (the launch allocation). Each role changes its budget

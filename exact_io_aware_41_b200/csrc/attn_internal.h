@@ -20,12 +20,15 @@ enum : unsigned int {
 // 8k x 8k head takes well under a millisecond), so reaching it means the pipeline is broken.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
-// Packed sequences: one block of query rows of one sequence, as the plan kernel lists them.
+// Packed sequences: one block of one sequence, as the plan lists them. Forward: a block of query rows, q_row and nq
+// from its first row on. Backward: a block of keys, k_row and nkv from its first key on.
 struct __align__(16) VarUnit {
-  int q_row;  // packed row of the block's first query
+  int q_row;  // packed row of the first query
   int nq;     // the sequence's queries from that row on
-  int k_row;  // packed row of the sequence's first key
-  int nkv;    // its keys
+  int k_row;  // packed row of the first key
+  int nkv;    // the sequence's keys from that row on
+  int seq;
+  int pad[3];
 };
 
 struct FwdArgs {
@@ -98,7 +101,7 @@ attn_status_t fwd_fp8_dispatch(const void* q8, const void* k8, const void* vt8, 
 // The plan of a packed call, in its workspace (attn_varlen.cu).
 struct VarPlan {
   VarUnit* units;        // [max_blocks]
-  int* count;            // blocks listed
+  int* count;            // blocks listed (-1: the offsets were out of order, nothing is to be written)
   unsigned int* claim;   // 0 when the plan is made
   long long max_blocks;
 };
@@ -109,6 +112,10 @@ attn_status_t fwd_varlen_dispatch(const VarPlan& plan, const void* q, const void
 attn_status_t fp8_quantize_dispatch(const void* x, const float* signs, void* codes, float* amax, int B, int N, int H,
                                     int transpose, cudaStream_t stream);
 
+attn_status_t bwd_varlen_launch(const VarPlan& plan, const void* q, const void* k, const void* v, const void* dout,
+                                void* dk, void* dv, float* acc, long long acc_rows, const float* lse2, const float* dd,
+                                long long lse_rows, int Tq, int Tk, int Hq, int Hkv, long long qs, long long ks,
+                                long long vs, float scale, int causal, cudaStream_t stream);
 size_t bwd_workspace(int B, int Hq, int Nq, int d);
 attn_status_t bwd_dispatch(const void* q, const void* k, const void* v, const void* o, const float* lse,
                            const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Nq, int Nkv,

@@ -24,18 +24,36 @@ struct PlanSeq {
   int q0, nq, k0, nkv;
 };
 
-// Tiles of 128 keys that forward block `blk` of a sequence walks (0: none of its rows sees a key).
-__device__ __forceinline__ int fwd_block_tiles(const PlanSeq& s, int blk, int causal) {
-  const int left = s.nq - blk * kFwdBlockRows;
-  const int end = causal ? min(s.nkv, min(kFwdBlockRows, left) + s.nkv - left) : s.nkv;
-  return end > 0 ? (end + kTileRows - 1) / kTileRows : 0;
-}
+// Forward: blocks of query rows, and the tiles of 128 keys that block `blk` walks (0: none of its rows sees a key).
+struct PlanFwd {
+  static __device__ __forceinline__ int blocks(const PlanSeq& s) { return (s.nq + kFwdBlockRows - 1) / kFwdBlockRows; }
+  static __device__ __forceinline__ int longest(const PlanSeq& s) { return (s.nkv + kTileRows - 1) / kTileRows; }
+  static __device__ __forceinline__ int tiles(const PlanSeq& s, int blk, int causal) {
+    const int left = s.nq - blk * kFwdBlockRows;
+    const int end = causal ? min(s.nkv, min(kFwdBlockRows, left) + s.nkv - left) : s.nkv;
+    return end > 0 ? (end + kTileRows - 1) / kTileRows : 0;
+  }
+  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk) {
+    return VarUnit{s.q0 + blk * kFwdBlockRows, s.nq - blk * kFwdBlockRows, s.k0, s.nkv, seq, {0, 0, 0}};
+  }
+};
+// Backward: blocks of 128 keys, and the tiles of 128 query rows that block `blk` walks.
+struct PlanBwd {
+  static __device__ __forceinline__ int blocks(const PlanSeq& s) { return (s.nkv + kTileRows - 1) / kTileRows; }
+  static __device__ __forceinline__ int longest(const PlanSeq& s) { return (s.nq + kTileRows - 1) / kTileRows; }
+  static __device__ __forceinline__ int tiles(const PlanSeq& s, int blk, int causal) {
+    return max(0, longest(s) - first_q_tile(causal, s.nq, s.nkv - blk * kTileRows));
+  }
+  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk) {
+    return VarUnit{s.q0, s.nq, s.k0 + blk * kTileRows, s.nkv - blk * kTileRows, seq, {0, 0, 0}};
+  }
+};
 
-__global__ void __launch_bounds__(kPlanThreads)
-    varlen_plan_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S, int Tq, int Tk,
-                       int causal, VarPlan plan) {
+// The plan, by one block of kPlanThreads threads.
+template <class P>
+__device__ __forceinline__ void make_plan(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S,
+                                          int Tq, int Tk, int causal, const VarPlan& plan) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch();
   // ---- check the offsets, and the largest number of tiles
   __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32], most;
   if (threadIdx.x == 0) most = 0;
@@ -45,12 +63,12 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int s = threadIdx.x; s < S; s += kPlanThreads) {
     const int a = cu_q[s], b = cu_q[s + 1], c = cu_k[s], e = cu_k[s + 1];
     bad |= a < 0 || b < a || b > Tq || c < 0 || e < c || e > Tk;
-    mx = max(mx, e - c);
+    mx = max(mx, P::longest(PlanSeq{a, b - a, c, e - c}));
   }
   bad = __syncthreads_or(bad);
   if (bad) {
     if (threadIdx.x == 0) {
-      *plan.count = 0;
+      *plan.count = -1;
       *plan.claim = 0;
       atomicOr(&g_error_word, kErrBadLengthBit);
     }
@@ -59,11 +77,11 @@ __global__ void __launch_bounds__(kPlanThreads)
   mx = __reduce_max_sync(0xffffffffu, mx);
   if (lane == 0) atomicMax(&most, mx);
   __syncthreads();
-  const int max_tiles = (most + kTileRows - 1) / kTileRows;
+  const int max_tiles = most;
   auto bin_of = [&](int tiles) -> int {  // 0: heaviest
     return max_tiles < kPlanBins ? max_tiles - tiles : int((long long)(max_tiles - tiles) * (kPlanBins - 1) / max_tiles);
   };
-  // f(sequence, block) for every block: a thread takes a sequence, a warp one with many blocks
+  // f(number of the sequence, sequence, block) for every block: a thread takes a sequence, a warp one with many blocks
   auto each_block = [&](auto f) {
     for (int s0 = warp * 32; s0 < S; s0 += kPlanThreads) {
       const int s = s0 + lane;
@@ -74,19 +92,19 @@ __global__ void __launch_bounds__(kPlanThreads)
         q.k0 = cu_k[s];
         q.nkv = cu_k[s + 1] - q.k0;
       }
-      const int nb = (q.nq + kFwdBlockRows - 1) / kFwdBlockRows;
+      const int nb = P::blocks(q);
       if (nb <= kPlanOwnBlocks)
-        for (int i = 0; i < nb; ++i) f(q, i);
+        for (int i = 0; i < nb; ++i) f(s, q, i);
       for (unsigned many = __ballot_sync(0xffffffffu, nb > kPlanOwnBlocks); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const PlanSeq w = {__shfl_sync(0xffffffffu, q.q0, src), __shfl_sync(0xffffffffu, q.nq, src),
                            __shfl_sync(0xffffffffu, q.k0, src), __shfl_sync(0xffffffffu, q.nkv, src)};
         const int wnb = __shfl_sync(0xffffffffu, nb, src);
-        for (int i = lane; i < wnb; i += 32) f(w, i);
+        for (int i = lane; i < wnb; i += 32) f(s0 + src, w, i);
       }
     }
   };
-  each_block([&](const PlanSeq& q, int i) { atomicAdd(&bins[bin_of(fwd_block_tiles(q, i, causal))], 1); });
+  each_block([&](int, const PlanSeq& q, int i) { atomicAdd(&bins[bin_of(P::tiles(q, i, causal))], 1); });
   __syncthreads();
   // exclusive scan of the bins
   const int mine = bins[threadIdx.x];
@@ -106,21 +124,23 @@ __global__ void __launch_bounds__(kPlanThreads)
     *plan.claim = 0;
   }
   __syncthreads();
-  each_block([&](const PlanSeq& q, int i) {
-    const int at = atomicAdd(&bins[bin_of(fwd_block_tiles(q, i, causal))], 1);
-    if (at >= plan.max_blocks) return;
-    VarUnit u;
-    u.q_row = q.q0 + i * kFwdBlockRows;
-    u.nq = q.nq - i * kFwdBlockRows;
-    u.k_row = q.k0;
-    u.nkv = q.nkv;
-    plan.units[at] = u;
+  each_block([&](int seq, const PlanSeq& q, int i) {
+    const int at = atomicAdd(&bins[bin_of(P::tiles(q, i, causal))], 1);
+    if (at < plan.max_blocks) plan.units[at] = P::unit(q, seq, i);
   });
 }
 static_assert(kPlanBins == kPlanThreads, "one bin per thread");
 
+__global__ void __launch_bounds__(kPlanThreads)
+    varlen_plan_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S, int Tq, int Tk,
+                       int causal, VarPlan plan) {
+  pdl_launch();
+  make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+}
+
 // Workspace of a plan: count and claim counter, blocks.
 long long fwd_max_blocks(int S, int Tq) { return (long long)Tq / kFwdBlockRows + S; }
+long long bwd_max_blocks(int S, int Tk) { return (long long)Tk / kTileRows + S; }
 size_t plan_bytes(long long max_blocks) { return 256 + (size_t(max_blocks) * sizeof(VarUnit) + 255) / 256 * 256; }
 
 VarPlan plan_at(void* workspace, long long max_blocks) {
@@ -131,22 +151,6 @@ VarPlan plan_at(void* workspace, long long max_blocks) {
   p.units = reinterpret_cast<VarUnit*>(w + 256);
   p.max_blocks = max_blocks;
   return p;
-}
-
-// 1 in ok[0] if both offset arrays are in order, else 0 and the error bit.
-__global__ void __launch_bounds__(1024) varlen_check_kernel(const int32_t* __restrict__ cu_q,
-                                                            const int32_t* __restrict__ cu_k, int S, int Tq, int Tk,
-                                                            int* ok) {
-  bool bad = false;
-  for (int s = threadIdx.x; s < S; s += blockDim.x) {
-    const int a = cu_q[s], b = cu_q[s + 1], c = cu_k[s], e = cu_k[s + 1];
-    bad |= a < 0 || b < a || b > Tq || c < 0 || e < c || e > Tk;
-  }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) {
-    *ok = bad ? 0 : 1;
-    if (bad) atomicOr(&g_error_word, kErrBadLengthBit);
-  }
 }
 
 // The sequence that owns packed row t (-1: none): the last s with cu[s] <= t, if t < cu[s + 1].
@@ -163,93 +167,113 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int S, int t) {
   return lo;
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-struct VarArgs {
-  const __nv_bfloat16 *q, *k, *v, *o, *dout;
-  const int32_t *cu_q, *cu_k;
-  __nv_bfloat16 *out, *dq, *dk, *dv;
-  float* lse;
-  const int* ok;
-  int S, Tq, Tk, Hq, Hkv;
-  long long qs, ks, vs;
-  float scale;
-  int causal;
+// ---- backward: pre- and post-pass ------------------------------------------------------------------------
+// The workspace after the plan: the fp32 dQ accumulator [acc_rows, Hq, 128] and per head the LSE' and D rows
+// [Hq, lse_rows], in which every sequence starts at a box or tile of its own (padded_row), and the accumulator
+// row of each packed row (-1: of no sequence).
+struct BwdSpace {
+  float* acc;
+  float* lse2;
+  float* dd;
+  int32_t* row_of;
+  long long acc_rows, lse_rows;
 };
 
-template <int D>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int lane, float* x) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = __bfloat162float(p[lane + 32 * i]);
-}
-
-__global__ void __launch_bounds__(256) varlen_dq_simple_kernel(const VarArgs a) {
-  constexpr int D = 128;
-  const int lane = threadIdx.x & 31;
-  const long long w = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5;
-  if (*a.ok == 0 || w >= (long long)a.Tq * a.Hq) return;
-  const int t = int(w / a.Hq), h = int(w % a.Hq), g = h / (a.Hq / a.Hkv);
-  const int s = seq_of_row(a.cu_q, a.S, t);
-  if (s < 0) return;
-  const int i = t - a.cu_q[s], nq = a.cu_q[s + 1] - a.cu_q[s], k0 = a.cu_k[s], nk = a.cu_k[s + 1] - k0;
-  const int end = a.causal ? min(nk, i + nk - nq + 1) : nk;
-  const size_t row = (size_t(t) * a.Hq + h) * D;
-  float q[4], o[4], g_o[4], k[4], v[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-  load_row<D>(a.q + t * a.qs + h * D, lane, q);
-  load_row<D>(a.o + row, lane, o);
-  load_row<D>(a.dout + row, lane, g_o);
-  const float dd = warp_sum(o[0] * g_o[0] + o[1] * g_o[1] + o[2] * g_o[2] + o[3] * g_o[3]);
-  const float L = a.lse[size_t(h) * a.Tq + t];
-  for (int j = 0; j < end; ++j) {
-    load_row<D>(a.k + (k0 + j) * a.ks + g * D, lane, k);
-    load_row<D>(a.v + (k0 + j) * a.vs + g * D, lane, v);
-    const float x = warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]) * a.scale;
-    const float dp = warp_sum(g_o[0] * v[0] + g_o[1] * v[1] + g_o[2] * v[2] + g_o[3] * v[3]);
-    const float ds = expf(x - L) * (dp - dd);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = fmaf(ds, k[e], acc[e]);
+// Block 0 makes the plan. The others take a packed query row per warp, 16 lanes per head: D = sum_e dO_e O_e and
+// LSE' = LSE log2 e (+inf for a row without keys, so that its P is 0), and the row of the accumulator zeroed, with
+// the padding rows of its last box after a sequence's last row. Every place a row of a sequence writes to lies
+// inside the arrays whatever the other offsets are; offsets out of order leave results unused (the plan says so).
+__global__ void __launch_bounds__(kPlanThreads)
+    varlen_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
+                          const float* __restrict__ lse, const int32_t* __restrict__ cu_q,
+                          const int32_t* __restrict__ cu_k, int S, int Tq, int Tk, int Hq, int causal, VarPlan plan,
+                          BwdSpace w) {
+  pdl_launch();
+  if (blockIdx.x == 0) {
+    make_plan<PlanBwd>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+    return;
   }
+  const int lane = threadIdx.x & 31, seg = lane & 15;
+  const int n_warps = int(gridDim.x - 1) * (kPlanThreads / 32);
+  for (long long t = (blockIdx.x - 1ll) * (kPlanThreads / 32) + (threadIdx.x >> 5); t < Tq; t += n_warps) {
+    int s = seq_of_row(cu_q, S, int(t));
+    const int first = s < 0 ? -1 : cu_q[s];
+    if (first < 0) s = -1;
+    const int i = int(t) - first;
+    const size_t acc_row = s < 0 ? 0 : padded_row(first, s, kAccRows) + i;
+    if (lane == 0) w.row_of[t] = s < 0 ? -1 : int(acc_row);
+    if (s < 0) continue;
+    const size_t lse_row = padded_row(first, s, kTileRows) + i;
+    const int zero_rows = i + 1 == cu_q[s + 1] - first ? (i / kAccRows + 1) * kAccRows - i : 1;
+    for (int h0 = 0; h0 < Hq; h0 += 2) {
+      const int h = h0 + (lane >> 4);
+      const bool real = h < Hq;
+      float dsum = 0.f;
+      if (real) {
+        const size_t row = (size_t(t) * Hq + h) * bwd::D;
+        const uint4 a = reinterpret_cast<const uint4*>(o + row)[seg];
+        const uint4 c = reinterpret_cast<const uint4*>(dout + row)[seg];
+        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) a.dq[row + lane + 32 * e] = __float2bfloat16_rn(acc[e] * a.scale);
-}
-
-__global__ void __launch_bounds__(256) varlen_dkv_simple_kernel(const VarArgs a) {
-  constexpr int D = 128;
-  const int lane = threadIdx.x & 31;
-  const long long w = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5;
-  if (*a.ok == 0 || w >= (long long)a.Tk * a.Hkv) return;
-  const int t = int(w / a.Hkv), g = int(w % a.Hkv), G = a.Hq / a.Hkv;
-  const int s = seq_of_row(a.cu_k, a.S, t);
-  if (s < 0) return;
-  const int j = t - a.cu_k[s], nk = a.cu_k[s + 1] - a.cu_k[s], q0 = a.cu_q[s], nq = a.cu_q[s + 1] - q0;
-  float k[4], v[4], q[4], o[4], g_o[4], dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  load_row<D>(a.k + t * a.ks + g * D, lane, k);
-  load_row<D>(a.v + t * a.vs + g * D, lane, v);
-  for (int i = a.causal ? max(0, j - (nk - nq)) : 0; i < nq; ++i)
-    for (int h = g * G; h < (g + 1) * G; ++h) {
-      const size_t row = (size_t(q0 + i) * a.Hq + h) * D;
-      load_row<D>(a.q + (q0 + i) * a.qs + h * D, lane, q);
-      load_row<D>(a.o + row, lane, o);
-      load_row<D>(a.dout + row, lane, g_o);
-      const float x = warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]) * a.scale;
-      const float dd = warp_sum(o[0] * g_o[0] + o[1] * g_o[1] + o[2] * g_o[2] + o[3] * g_o[3]);
-      const float dp = warp_sum(g_o[0] * v[0] + g_o[1] * v[1] + g_o[2] * v[2] + g_o[3] * v[3]);
-      const float p = expf(x - a.lse[size_t(h) * a.Tq + q0 + i]), ds = p * (dp - dd);
+        for (int k = 0; k < 4; ++k) {
+          dsum = fmaf(__uint_as_float(wa[k] << 16), __uint_as_float(wc[k] << 16), dsum);
+          dsum = fmaf(__uint_as_float(wa[k] & 0xFFFF0000u), __uint_as_float(wc[k] & 0xFFFF0000u), dsum);
+        }
+        for (int r = 0; r < zero_rows; ++r) {
+          float4* z = reinterpret_cast<float4*>(w.acc + ((acc_row + r) * Hq + h) * bwd::D) + 2 * seg;
+          z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+          z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dv[e] = fmaf(p, g_o[e], dv[e]);
-        dk[e] = fmaf(ds, q[e], dk[e]);
+      for (int off = 8; off > 0; off >>= 1) dsum += __shfl_xor_sync(0xffffffffu, dsum, off);
+      if (real && seg == 0) {
+        const float L = lse[size_t(h) * Tq + t];
+        w.lse2[h * w.lse_rows + lse_row] = (L == -INFINITY) ? INFINITY : L * 1.4426950408889634f;
+        w.dd[h * w.lse_rows + lse_row] = dsum;
       }
     }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    a.dk[(size_t(t) * a.Hkv + g) * D + lane + 32 * e] = __float2bfloat16_rn(dk[e] * a.scale);
-    a.dv[(size_t(t) * a.Hkv + g) * D + lane + 32 * e] = __float2bfloat16_rn(dv[e]);
   }
+}
+
+// dQ = scale * accumulator, bf16, for the rows that a sequence owns
+__global__ void __launch_bounds__(256)
+    varlen_bwd_post_kernel(const int* count, const float* acc, const int32_t* row_of, __nv_bfloat16* __restrict__ dq,
+                           int Tq, int Hq, float scale) {
+  pdl_wait();
+  if (*count < 0) return;
+  const int per_row = Hq * (bwd::D / 4);
+  const size_t n4 = size_t(Tq) * per_row;
+  for (size_t i = blockIdx.x * size_t(blockDim.x) + threadIdx.x; i < n4; i += size_t(gridDim.x) * blockDim.x) {
+    const int t = int(i / per_row), e = int(i % per_row), r = row_of[t];
+    if (r < 0) continue;
+    const float4 v = reinterpret_cast<const float4*>(acc)[size_t(r) * per_row + e];
+    uint2 x;
+    x.x = pack_bf16x2(v.x * scale, v.y * scale);
+    x.y = pack_bf16x2(v.z * scale, v.w * scale);
+    reinterpret_cast<uint2*>(dq)[i] = x;
+  }
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The backward workspace: its size (workspace null), or where its parts are.
+size_t bwd_space(void* workspace, int S, int Tq, int Tk, int Hq, VarPlan* plan, BwdSpace* w) {
+  const long long max_blocks = bwd_max_blocks(S, Tk);
+  w->acc_rows = ((long long)Tq / kAccRows + S) * kAccRows;
+  w->lse_rows = ((long long)Tq / kTileRows + S) * kTileRows;
+  const size_t acc = up256(plan_bytes(max_blocks)), lse2 = acc + up256(size_t(w->acc_rows) * Hq * bwd::D * sizeof(float)),
+               dd = lse2 + up256(size_t(w->lse_rows) * Hq * sizeof(float)),
+               row_of = dd + up256(size_t(w->lse_rows) * Hq * sizeof(float));
+  if (workspace != nullptr) {
+    char* b = static_cast<char*>(workspace);
+    *plan = plan_at(workspace, max_blocks);
+    w->acc = reinterpret_cast<float*>(b + acc);
+    w->lse2 = reinterpret_cast<float*>(b + lse2);
+    w->dd = reinterpret_cast<float*>(b + dd);
+    w->row_of = reinterpret_cast<int32_t*>(b + row_of);
+  }
+  return row_of + up256(size_t(Tq) * sizeof(int32_t));
 }
 
 // Rows `stride` elements apart that hold heads * d dense elements: 16-byte aligned rows, and byte offsets
@@ -275,8 +299,6 @@ attn_status_t varlen_args_status(const void* const* ptrs16, int n, const float* 
   if (S > kVarMaxSeqs) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
-
-unsigned warps_grid(long long warps) { return unsigned((warps + 7) / 8); }
 }  // namespace
 
 }  // namespace attn
@@ -312,7 +334,9 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const
 
 size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d) {
   if (S < 1 || Tq < 1 || Tk < 1 || Hq < 1 || d < 1 || S > kVarMaxSeqs) return 0;
-  return 256;
+  VarPlan plan;
+  BwdSpace w;
+  return bwd_space(nullptr, S, Tq, Tk, Hq, &plan, &w);
 }
 
 attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -328,33 +352,39 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d))
     return ATTN_ERR_WORKSPACE;
-  VarArgs a = {};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k);
-  a.v = static_cast<const __nv_bfloat16*>(v);
-  a.o = static_cast<const __nv_bfloat16*>(o);
-  a.dout = static_cast<const __nv_bfloat16*>(dout);
-  a.cu_q = cu_q;
-  a.cu_k = cu_k;
-  a.dq = static_cast<__nv_bfloat16*>(dq);
-  a.dk = static_cast<__nv_bfloat16*>(dk);
-  a.dv = static_cast<__nv_bfloat16*>(dv);
-  a.lse = const_cast<float*>(lse);
-  a.ok = static_cast<int*>(workspace);
-  a.S = S;
-  a.Tq = Tq;
-  a.Tk = Tk;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.qs = q_stride;
-  a.ks = k_stride;
-  a.vs = v_stride;
-  a.scale = scale;
-  a.causal = causal;
-  varlen_check_kernel<<<1, 1024, 0, stream>>>(cu_q, cu_k, S, Tq, Tk, static_cast<int*>(workspace));
-  varlen_dq_simple_kernel<<<warps_grid((long long)Tq * Hq), 256, 0, stream>>>(a);
-  varlen_dkv_simple_kernel<<<warps_grid((long long)Tk * Hkv), 256, 0, stream>>>(a);
-  return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : (cudaGetLastError(), ATTN_ERR_CUDA);
+  VarPlan plan;
+  BwdSpace w;
+  bwd_space(workspace, S, Tq, Tk, Hq, &plan, &w);
+  // tile coordinates, and the grid, are 32-bit
+  if (plan.max_blocks * Hkv > 0x7FFFFFFFll || w.acc_rows > 0x7FFFFFFFll || w.lse_rows > 0x7FFFFFFFll)
+    return ATTN_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  // a warp per row, at most two blocks of them per SM
+  const long long want = ((long long)Tq + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
+  const unsigned rows_grid = unsigned(want < 2ll * sms ? want : 2ll * sms);
+  varlen_bwd_pre_kernel<<<1 + rows_grid, kPlanThreads, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, cu_q, cu_k, S, Tq, Tk, Hq,
+      causal, plan, w);
+  if (cudaPeekAtLastError() != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
+  st = bwd_varlen_launch(plan, q, k, v, dout, dk, dv, w.acc, w.acc_rows, w.lse2, w.dd, w.lse_rows, Tq, Tk, Hq, Hkv,
+                         q_stride, k_stride, v_stride, scale, causal, stream);
+  if (st != ATTN_OK) return st;
+  const size_t n4 = size_t(Tq) * Hq * bwd::D / 4;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(unsigned(n4 / 256 + 1 < 8192 ? n4 / 256 + 1 : 8192));
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, varlen_bwd_post_kernel, static_cast<const int*>(plan.count),
+                         static_cast<const float*>(w.acc), static_cast<const int32_t*>(w.row_of),
+                         static_cast<__nv_bfloat16*>(dq), Tq, Hq, scale) != cudaSuccess)
+    return cudaGetLastError(), ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 }  // extern "C"

