@@ -338,31 +338,35 @@ def attn_bwd(q, k, v, o, lse, dout, scale: float | None = None, causal: bool = F
 # ---- packed sequences and the paged cache --------------------------------------------------------------
 # These run on the device of their first tensor, whatever the current device is, and allocate what the
 # caller does not pass on the stream they run on, so that torch's allocator never hands that memory to
-# other work before the call is done with it.
+# other work before the call is done with it. The smallest calls take a few microseconds on the GPU, so the
+# checks below look at each tensor once and build no strings or contexts on the way of a call that is right.
 
-def _on(t, stream):
-    """Context in which allocations and the launch belong to t's device and the given stream."""
-    import contextlib
+def _elsewhere(device, stream):
+    """None if the call runs on the current device and stream, else the context it runs in."""
     import torch
 
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
 
 
-def _token_rows(name, t, ndim, device=None):
-    """Checks a bf16 [.., tokens, heads, d] operand whose tokens may be a stride apart; returns that stride."""
+def _current_stream(device) -> int:
     import torch
 
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != ndim:
-        raise ValueError(f"{name} must be a {ndim}-d bf16 CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _token_rows(name, t, bf16, device):
+    """Checks a bf16 [tokens, heads, d] operand whose tokens may be a stride apart; returns that stride."""
+    if t.dtype is not bf16 or t.dim() != 3 or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a 3-d bf16 CUDA tensor on {device}")
     n, h, d = t.shape
+    if t.is_contiguous():
+        return h * d
     sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
@@ -370,40 +374,29 @@ def _token_rows(name, t, ndim, device=None):
 
 
 def _dense(name, t, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
-def _int32(name, t, ndim, device):
-    import torch
-
-    if t.dtype != torch.int32 or t.device != device or t.dim() != ndim or not t.is_contiguous():
+def _indices(name, t, int32, ndim, device):
+    if t.dtype is not int32 or t.device != device or t.dim() != ndim or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {ndim}-d int32 tensor on {device}")
 
 
-def _workspace(workspace, need, device):
-    import torch
-
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+def _space(workspace, device):
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
 
 
-def _varlen_shapes(q, k, v, cu_q, cu_k):
-    dev = q.device
-    qs = _token_rows("q", q, 3)
-    ks = _token_rows("k", k, 3, dev)
-    vs = _token_rows("v", v, 3, dev)
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
-        raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
-    _int32("cu_seqlens_q", cu_q, 1, dev)
+def _offsets_of(cu_q, cu_k, int32, device):
+    """Number of sequences, after a look at both offset arrays."""
+    _indices("cu_seqlens_q", cu_q, int32, 1, device)
     if cu_k is not cu_q:
-        _int32("cu_seqlens_k", cu_k, 1, dev)
-    if cu_q.shape != cu_k.shape or cu_q.numel() < 2:
+        _indices("cu_seqlens_k", cu_k, int32, 1, device)
+    S = cu_q.shape[0] - 1
+    if S < 1 or cu_k.shape[0] != S + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have one entry more than there are sequences")
-    return dev, qs, ks, vs
+    return S
 
 
 def attn_fwd_varlen_workspace_bytes(S: int, Tq: int) -> int:
@@ -421,29 +414,39 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale: float | Non
     """
     import torch
 
+    dev = q.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, workspace, out, lse)
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
-    dev, qs, ks, vs = _varlen_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    bf16 = torch.bfloat16
+    qs = _token_rows("q", q, bf16, dev)
+    ks = _token_rows("k", k, bf16, dev)
+    vs = _token_rows("v", v, bf16, dev)
     Tq, Hq, d = q.shape
-    Tk, Hkv, _ = k.shape
-    S = cu_seqlens_q.numel() - 1
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    Tk, Hkv, dk = k.shape
+    if k.shape != v.shape or dk != d:
+        raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
+    S = _offsets_of(cu_seqlens_q, cu_seqlens_k, torch.int32, dev)
     lib = lib_handle()
-    with _on(q, stream):
-        if out is None:
-            out = torch.empty((Tq, Hq, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _dense("out", out, torch.bfloat16, (Tq, Hq, d), dev)
-        if lse is None:
-            lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
-        else:
-            _dense("lse", lse, torch.float32, (Hq, Tq), dev)
-        workspace = _workspace(workspace, lib.attn_fwd_varlen_workspace_bytes(S, Tq), dev)
-        code = lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
-                                   cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs,
-                                   ks, vs, float(scale), int(bool(causal)), workspace.data_ptr(), workspace.nbytes,
-                                   _stream(stream))
+    if out is None:
+        out = torch.empty((Tq, Hq, d), dtype=bf16, device=dev)
+    else:
+        _dense("out", out, bf16, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
+    else:
+        _dense("lse", lse, torch.float32, (Hq, Tq), dev)
+    if workspace is None:
+        workspace = torch.empty(lib.attn_fwd_varlen_workspace_bytes(S, Tq), dtype=torch.uint8, device=dev)
+    else:
+        _space(workspace, dev)
+    code = lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
+                               cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks,
+                               vs, d ** -0.5 if scale is None else scale, 1 if causal else 0, workspace.data_ptr(),
+                               workspace.nbytes, _current_stream(dev))
     _check("attn_fwd_varlen", code)
     return out, lse
 
@@ -458,47 +461,59 @@ def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k=None, scal
     returned them, dout [Tq, Hq, d] like o. Returns (dQ, dK, dV), dense, in the shapes of q, k, v."""
     import torch
 
+    dev = q.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale, causal, workspace, dq, dk,
+                                   dv)
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
-    dev, qs, ks, vs = _varlen_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k)
-    Tq, Hq, d = q.shape
-    Tk, Hkv, _ = k.shape
-    S = cu_seqlens_q.numel() - 1
     bf16 = torch.bfloat16
-    _dense("o", o, bf16, (Tq, Hq, d), dev)
-    _dense("dout", dout, bf16, (Tq, Hq, d), dev)
+    qs = _token_rows("q", q, bf16, dev)
+    ks = _token_rows("k", k, bf16, dev)
+    vs = _token_rows("v", v, bf16, dev)
+    Tq, Hq, d = q.shape
+    Tk, Hkv, d_k = k.shape
+    if k.shape != v.shape or d_k != d:
+        raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
+    S = _offsets_of(cu_seqlens_q, cu_seqlens_k, torch.int32, dev)
+    _dense("o", o, bf16, q.shape, dev)
+    _dense("dout", dout, bf16, q.shape, dev)
     _dense("lse", lse, torch.float32, (Hq, Tq), dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     lib = lib_handle()
-    with _on(q, stream):
-        grads = []
-        for name, g, shape in (("dq", dq, q.shape), ("dk", dk, k.shape), ("dv", dv, v.shape)):
-            if g is None:
-                g = torch.empty(shape, dtype=bf16, device=dev)
-            else:
-                _dense(name, g, bf16, shape, dev)
-            grads.append(g)
-        dq, dk, dv = grads
-        workspace = _workspace(workspace, lib.attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d), dev)
-        code = lib.attn_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                   dout.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), dq.data_ptr(),
-                                   dk.data_ptr(), dv.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks, vs, float(scale),
-                                   int(bool(causal)), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if dq is None:
+        dq = torch.empty_like(o)
+    else:
+        _dense("dq", dq, bf16, q.shape, dev)
+    if dk is None:
+        dk = torch.empty((Tk, Hkv, d), dtype=bf16, device=dev)
+    else:
+        _dense("dk", dk, bf16, k.shape, dev)
+    if dv is None:
+        dv = torch.empty_like(dk)
+    else:
+        _dense("dv", dv, bf16, k.shape, dev)
+    if workspace is None:
+        workspace = torch.empty(lib.attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d), dtype=torch.uint8, device=dev)
+    else:
+        _space(workspace, dev)
+    code = lib.attn_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                               dv.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
+                               1 if causal else 0, workspace.data_ptr(), workspace.nbytes, _current_stream(dev))
     _check("attn_bwd_varlen", code)
     return dq, dk, dv
 
 
-def _pool_shape(k_pages, v_pages, page_table, kv_lens, dev):
-    import torch
-
+def _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, int32, dev):
     for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous [n_pages, page_size, Hkv, d] bf16 tensor on {dev}")
+        if t.dtype is not bf16 or t.device != dev or t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous [n_pages, page_size, Hkv, d] bf16 CUDA tensor on {dev}")
     if k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
-    _int32("page_table", page_table, 2, dev)
-    _int32("kv_lens", kv_lens, 1, dev)
+    _indices("page_table", page_table, int32, 2, dev)
+    _indices("kv_lens", kv_lens, int32, 1, dev)
     if page_table.shape[0] != kv_lens.shape[0]:
         raise ValueError("page_table must be [B, max_pages] and kv_lens [B]")
     return k_pages.shape
@@ -519,28 +534,33 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_lens, scale: float | N
     import torch
 
     dev = q.device
-    qs = _token_rows("q", q, 3)
-    n_pages, page_size, Hkv, _ = _pool_shape(k_pages, v_pages, page_table, kv_lens, dev)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_decode_paged(q, k_pages, v_pages, page_table, kv_lens, scale, workspace, out, lse)
+    bf16 = torch.bfloat16
+    qs = _token_rows("q", q, bf16, dev)
+    n_pages, page_size, Hkv, d_k = _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, torch.int32, dev)
     B, Hq, d = q.shape
-    if k_pages.shape[3] != d or kv_lens.shape[0] != B:
+    if d_k != d or kv_lens.shape[0] != B:
         raise ValueError("k_pages must have q's d, kv_lens and page_table q's B")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     lib = lib_handle()
-    with _on(q, stream):
-        if out is None:
-            out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _dense("out", out, torch.bfloat16, (B, Hq, d), dev)
-        if lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        else:
-            _dense("lse", lse, torch.float32, (B, Hq), dev)
-        workspace = _workspace(workspace, lib.attn_decode_paged_workspace_bytes(B, Hq, Hkv, d), dev)
-        code = lib.attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                                     kv_lens.data_ptr(), n_pages, page_size, page_table.shape[1], out.data_ptr(),
-                                     lse.data_ptr(), B, Hq, Hkv, d, qs, float(scale), workspace.data_ptr(),
-                                     workspace.nbytes, _stream(stream))
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=bf16, device=dev)
+    else:
+        _dense("out", out, bf16, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    else:
+        _dense("lse", lse, torch.float32, (B, Hq), dev)
+    if workspace is None:
+        workspace = torch.empty(lib.attn_decode_paged_workspace_bytes(B, Hq, Hkv, d), dtype=torch.uint8, device=dev)
+    else:
+        _space(workspace, dev)
+    code = lib.attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                 kv_lens.data_ptr(), n_pages, page_size, page_table.shape[1], out.data_ptr(),
+                                 lse.data_ptr(), B, Hq, Hkv, d, qs, d ** -0.5 if scale is None else scale,
+                                 workspace.data_ptr(), workspace.nbytes, _current_stream(dev))
     _check("attn_decode_paged", code)
     return out, lse
 
@@ -549,21 +569,28 @@ def attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_se
     """Writes new rows of K and V [T, Hkv, d] into the pages of their sequences, in place. cu_seqlens int32
     [B + 1]: sequence b's new rows are cu[b] .. cu[b + 1) (None: one row per sequence, T = B); kv_lens int32 [B]
     are the lengths with the new rows, so the last of them becomes token kv_lens[b] - 1."""
+    import torch
+
     dev = k_pages.device
-    n_pages, page_size, Hkv, d = _pool_shape(k_pages, v_pages, page_table, kv_lens, dev)
-    ks = _token_rows("k_new", k_new, 3, dev)
-    vs = _token_rows("v_new", v_new, 3, dev)
-    T, B = k_new.shape[0], kv_lens.shape[0]
-    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (Hkv, d):
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens)
+    bf16 = torch.bfloat16
+    n_pages, page_size, Hkv, d = _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, torch.int32, dev)
+    ks = _token_rows("k_new", k_new, bf16, dev)
+    vs = _token_rows("v_new", v_new, bf16, dev)
+    T, H, dn = k_new.shape
+    B = kv_lens.shape[0]
+    if k_new.shape != v_new.shape or H != Hkv or dn != d:
         raise ValueError("k_new and v_new must be [T, Hkv, d] with the pool's Hkv and d")
+    cu = None
     if cu_seqlens is not None:
-        _int32("cu_seqlens", cu_seqlens, 1, dev)
+        _indices("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
         if cu_seqlens.shape[0] != B + 1:
             raise ValueError("cu_seqlens must be [B + 1]")
-    with _on(k_pages, stream):
-        code = lib_handle().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(),
-                                              None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                                              page_table.data_ptr(), kv_lens.data_ptr(), k_pages.data_ptr(),
-                                              v_pages.data_ptr(), B, T, n_pages, page_size, page_table.shape[1], Hkv, d,
-                                              ks, vs, _stream(stream))
+        cu = cu_seqlens.data_ptr()
+    code = lib_handle().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(), cu, page_table.data_ptr(),
+                                          kv_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, T, n_pages,
+                                          page_size, page_table.shape[1], Hkv, d, ks, vs, _current_stream(dev))
     _check("attn_cache_append", code)
