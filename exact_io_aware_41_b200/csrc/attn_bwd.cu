@@ -288,16 +288,23 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       constexpr uint32_t idesc_mnmn = idesc_bf16_f32(128, 128, 1, 1);  // A, B MN-major
       bool ok = mbar_wait(kv_full, 0, abort_flag, T);
       int tails = 0;  // tiles given to the tail warp (phase of t_clean)
+      // f(k-step) over the `rows` (at most 128) that a product sums over, 16 at a time
+      auto k_steps = [](int rows, auto f) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (!VL || kk * 16 < rows) f(kk);
+      };
       const int keys = VL ? min(nkv, BN) : BN;
+      const int last_queries = nq - (n_qt - 1) * BM;  // of each head's last tile
+      int until_last = steps_per_head;                // steps before it, counted down
       if (VL && ok && keys < BN) {
         mbar_arrive(t_land);
         ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
       }
       for (int t = 0; t < n_steps && ok; ++t) {
         const int st = t & 1;
-        int h, qt;
-        step_coords(t, h, qt);
-        const int queries = VL ? min(nq - qt * BM, BM) : BM;  // of this step's tile
+        if (VL && --until_last < 0) until_last = steps_per_head - 1;
+        const int queries = VL && until_last == 0 ? last_queries : BM;  // of this step's tile
         const uint32_t sq = smem_u32(smem + OFF_Q0 + 2 * st * TILE_BYTES);
         const uint64_t dQ_k = smem_desc(sq, 16, 1024, kLayoutSW128);
         const uint64_t dDO_k = smem_desc(sq + TILE_BYTES, 16, 1024, kLayoutSW128);
@@ -336,28 +343,22 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         if (VL && ok && queries < BM) ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < BM / 16; ++kk) {
-          if (VL && kk * 16 >= queries) break;
+        k_steps(queries, [&](int kk) {
           umma_ts(tmem + DV_COL, tmem + S_COL + 32 * (kk / 2) + 8 * (kk % 2),
                   dDO_mn + uint64_t((kk * 16 * 128) >> 4), idesc_tmn, (t > 0 || kk > 0) ? 1u : 0u);
-        }
+        });
         ok = mbar_wait(p_full, uint32_t(t & 1), abort_flag, T);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk) {
-          if (VL && kk * 16 >= keys) break;
+        k_steps(keys, [&](int kk) {
           umma_ss(tmem + S_COL, dDS_mn + uint64_t((kk * 16 * 128) >> 4), dK_mn + uint64_t((kk * 16 * 128) >> 4),
                   idesc_mnmn, kk > 0 ? 1u : 0u);
-        }
+        });
         umma_commit(dq_full);
-#pragma unroll
-        for (int kk = 0; kk < BM / 16; ++kk) {
-          if (VL && kk * 16 >= queries) break;
+        k_steps(queries, [&](int kk) {
           umma_ts(tmem + DK_COL, tmem + DP_COL + 32 * (kk / 2) + 8 * (kk % 2),
                   dQ_mn + uint64_t((kk * 16 * 128) >> 4), idesc_tmn, (t > 0 || kk > 0) ? 1u : 0u);
-        }
+        });
         umma_commit(&dk_done[t & 1]);
         if (t == n_steps - 1) umma_commit(dkv_full);
       }
@@ -493,12 +494,13 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag, T));
     };
     bool ok = true;
+    const int q_begin = qt0 * BM;  // the query tiles of a head are walked from here, head after head
+    int q0 = q_begin - BM;
     for (int t = 0; t < n_steps && ok; ++t) {
-      int h, qt;
-      step_coords(t, h, qt);
+      q0 += BM;
+      if (q0 >= nq) q0 = q_begin;
       const float* s_lse = reinterpret_cast<const float*>(smem + OFF_LSE0 + (t & 1) * 1024);
       const float* s_dd = s_lse + 128;
-      const int q0 = qt * BM;
       // P first, from S^T alone (its product is done before dP^T's), kept in fp32 for dS
       if (!wait_warp(st_full, uint32_t(t & 1))) {
         ok = false;
@@ -529,13 +531,24 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
             const float2 x = ffma2(make_float2(__uint_as_float(sv[4 * i4 + u]), __uint_as_float(sv[4 * i4 + u + 1])),
                                    make_float2(c, c), make_float2(-lv[u], -lv[u + 1]));
             float2 p = make_float2(ex2(x.x), ex2(x.y));
-            if (need_mask) {
-              if (!(key_ok && (!args.causal || key <= q0 + qi + diag) && (!VL || q0 + qi < nq))) p.x = 0.f;
-              if (!(key_ok && (!args.causal || key <= q0 + qi + 1 + diag) && (!VL || q0 + qi + 1 < nq))) p.y = 0.f;
+            if (!VL && need_mask) {
+              if (!(key_ok && (!args.causal || key <= q0 + qi + diag))) p.x = 0.f;
+              if (!(key_ok && (!args.causal || key <= q0 + qi + 1 + diag))) p.y = 0.f;
             }
             pf[cx][4 * i4 + u] = p.x;
             pf[cx][4 * i4 + u + 1] = p.y;
             pk[2 * i4 + h2] = pack_bf16x2(p.x, p.y);
+          }
+        }
+        if (VL && need_mask) {
+          // the same after the fact, in a pass of its own, so that whole tiles pay nothing for it: queries
+          // [first, left) of this chunk see this key
+          const int first = args.causal ? key - diag - qf : 0, left = key_ok ? nq - qf : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (2 * i < first || 2 * i >= left) pf[cx][2 * i] = 0.f;
+            if (2 * i + 1 < first || 2 * i + 1 >= left) pf[cx][2 * i + 1] = 0.f;
+            pk[i] = pack_bf16x2(pf[cx][2 * i], pf[cx][2 * i + 1]);
           }
         }
         // P^T over S^T, bf16 pairs: the chunk's 16 columns go to the first 16 of its own 32 score
@@ -561,8 +574,6 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         tmem_ld_wait();
         tmem_reg_fence32(dpv);
         uint32_t dk2[16];
-        // packed: keys and queries of other sequences, where dP may be anything (P = 0 there)
-        const bool foreign = VL && (BN > nkv || q0 + cc * 32 + 32 > nq);
 #pragma unroll
         for (int i4 = 0; i4 < 8; ++i4) {
           const float4 d4 = *reinterpret_cast<const float4*>(s_dd + cc * 32 + 4 * i4);
@@ -570,16 +581,19 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const int u = 2 * h2;
-            float2 ds = fmul2(make_float2(pf[cx][4 * i4 + u], pf[cx][4 * i4 + u + 1]),
-                              fadd2(make_float2(__uint_as_float(dpv[4 * i4 + u]), __uint_as_float(dpv[4 * i4 + u + 1])),
-                                    make_float2(-dv4[u], -dv4[u + 1])));
-            if (foreign) {
-              const int qi = q0 + cc * 32 + 4 * i4 + u;
-              if (!key_ok || qi >= nq) ds.x = 0.f;
-              if (!key_ok || qi + 1 >= nq) ds.y = 0.f;
-            }
+            const float2 ds = fmul2(make_float2(pf[cx][4 * i4 + u], pf[cx][4 * i4 + u + 1]),
+                                    fadd2(make_float2(__uint_as_float(dpv[4 * i4 + u]), __uint_as_float(dpv[4 * i4 + u + 1])),
+                                          make_float2(-dv4[u], -dv4[u + 1])));
             dk2[2 * i4 + h2] = pack_bf16x2(ds.x, ds.y);
           }
+        }
+        // packed: keys and queries of other sequences, where dP may be anything (P = 0 there); a pass of its own
+        // over the packed pairs, so that whole tiles pay nothing for it
+        if (VL && (BN > nkv || q0 + cc * 32 + 32 > nq)) {
+          const int left = key_ok ? nq - (q0 + cc * 32) : 0;  // queries of this chunk that count for this key
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            dk2[i] = 2 * i + 1 < left ? dk2[i] : 2 * i < left ? dk2[i] & 0xFFFFu : 0u;
         }
         // dS^T over dP^T, as P^T over S^T
         tmem_st16(lane_addr + DP_COL + cc * 32, dk2);
