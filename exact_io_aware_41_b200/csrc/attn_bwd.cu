@@ -139,7 +139,7 @@ __device__ __forceinline__ int first_q_tile(int causal, int nq, int nkv) {
 
 // VL: packed sequences. A key block, and the query tiles it walks, belong to one sequence; tiles that reach past
 // its end hold rows of the next sequence, which are masked where they are rows or columns of a product, and
-// zeroed (or left out, by whole k-steps) where a product sums over them.
+// zeroed where a product sums over them.
 template <bool VL>
 __global__ void __launch_bounds__(bwd::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
   if constexpr (VL) {
     pdl_wait();  // the pre-pass, with the plan, is in memory
     pdl_launch();
-    if (kb >= *args.var_count) return;  // (the grid is sized by a bound)
-    const VarUnit u = args.var_units[kb];
+    const VarUnit u = args.var_units[kb];  // (read with the count; entries behind it hold nothing)
+    if (kb >= *args.var_count) return;     // (the grid is sized by a bound)
     k_row = u.k_row;
     nkv = u.nkv;
     q_row = u.q_row;
@@ -288,23 +288,16 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       constexpr uint32_t idesc_mnmn = idesc_bf16_f32(128, 128, 1, 1);  // A, B MN-major
       bool ok = mbar_wait(kv_full, 0, abort_flag, T);
       int tails = 0;  // tiles given to the tail warp (phase of t_clean)
-      // f(k-step) over the `rows` (at most 128) that a product sums over, 16 at a time
-      auto k_steps = [](int rows, auto f) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (!VL || kk * 16 < rows) f(kk);
-      };
-      const int keys = VL ? min(nkv, BN) : BN;
-      const int last_queries = nq - (n_qt - 1) * BM;  // of each head's last tile
-      int until_last = steps_per_head;                // steps before it, counted down
-      if (VL && ok && keys < BN) {
+      // steps up to the next one whose query tile is cut off (each head's last; never, if it is whole)
+      int until_cut = VL && nq % BM != 0 ? steps_per_head : 0x7FFFFFFF;
+      if (VL && ok && nkv < BN) {
         mbar_arrive(t_land);
         ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
       }
       for (int t = 0; t < n_steps && ok; ++t) {
         const int st = t & 1;
-        if (VL && --until_last < 0) until_last = steps_per_head - 1;
-        const int queries = VL && until_last == 0 ? last_queries : BM;  // of this step's tile
+        const bool cut = VL && --until_cut == 0;
+        if (cut) until_cut = steps_per_head;
         const uint32_t sq = smem_u32(smem + OFF_Q0 + 2 * st * TILE_BYTES);
         const uint64_t dQ_k = smem_desc(sq, 16, 1024, kLayoutSW128);
         const uint64_t dDO_k = smem_desc(sq + TILE_BYTES, 16, 1024, kLayoutSW128);
@@ -312,7 +305,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         const uint64_t dDO_mn = smem_desc(sq + TILE_BYTES, CHUNK_BYTES, 1024, kLayoutSW128);
         ok = mbar_wait(&q_full[st], uint32_t((t >> 1) & 1), abort_flag, T);
         if (!ok) break;
-        if (VL && queries < BM) mbar_arrive(t_land);
+        if (cut) mbar_arrive(t_land);
         tc_fence_after();
         // S^T = K Q^T into [0, 128), once the previous step's dQ (there) has been read out
         if (t > 0) {
@@ -340,25 +333,25 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
         // A = P^T / dS^T: queries 16kk .. 16kk+15 are columns 8 (kk % 2) .. of chunk kk / 2, which
         // starts at column 32 (kk / 2)
         ok = mbar_wait(pt_full, uint32_t(t & 1), abort_flag, T);
-        if (VL && ok && queries < BM) ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
+        if (cut && ok) ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
         if (!ok) break;
         tc_fence_after();
-        k_steps(queries, [&](int kk) {
+#pragma unroll
+        for (int kk = 0; kk < BM / 16; ++kk)
           umma_ts(tmem + DV_COL, tmem + S_COL + 32 * (kk / 2) + 8 * (kk % 2),
                   dDO_mn + uint64_t((kk * 16 * 128) >> 4), idesc_tmn, (t > 0 || kk > 0) ? 1u : 0u);
-        });
         ok = mbar_wait(p_full, uint32_t(t & 1), abort_flag, T);
         if (!ok) break;
         tc_fence_after();
-        k_steps(keys, [&](int kk) {
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
           umma_ss(tmem + S_COL, dDS_mn + uint64_t((kk * 16 * 128) >> 4), dK_mn + uint64_t((kk * 16 * 128) >> 4),
                   idesc_mnmn, kk > 0 ? 1u : 0u);
-        });
         umma_commit(dq_full);
-        k_steps(queries, [&](int kk) {
+#pragma unroll
+        for (int kk = 0; kk < BM / 16; ++kk)
           umma_ts(tmem + DK_COL, tmem + DP_COL + 32 * (kk / 2) + 8 * (kk % 2),
                   dQ_mn + uint64_t((kk * 16 * 128) >> 4), idesc_tmn, (t > 0 || kk > 0) ? 1u : 0u);
-        });
         umma_commit(&dk_done[t & 1]);
         if (t == n_steps - 1) umma_commit(dkv_full);
       }
@@ -375,15 +368,14 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     if (VL && warp == 3) {
       // ================================ tail rows ================================
       // dV, dK sum over the queries of a tile and dQ over its keys: P = dS = 0 does not cancel NaN or infinities in
-      // rows of the next sequence, so those that share the last k-step with the sequence's rows are zeroed once
-      // the tile has landed, while the elementwise warps work. The phases of t_land may lie many steps apart,
+      // rows of the next sequence, so those are zeroed once the tile has landed, while the elementwise warps work. The phases of t_land may lie many steps apart,
       // whose own waits are bounded and end this one, hence its own limit.
       constexpr uint64_t kTailLimit = 512 * kWaitLimitNs;
       int tails = 0;
-      // zeroes rows [cut, next multiple of 16) of n tiles at `tile`, once the next phase of t_land is there
+      // zeroes rows [cut, 128) of n tiles at `tile`, once the next phase of t_land is there
       auto clean = [&](uint8_t* tile, int n, int cut) -> bool {
         if (!__all_sync(0xffffffffu, mbar_wait(t_land, uint32_t(tails++ & 1), abort_flag, kTailLimit))) return false;
-        const int rows = (16 - cut % 16) % 16;
+        const int rows = 128 - cut;
         for (int i = lane; i < n * rows * 16; i += 32) {
           const int r = cut + (i / 16) % rows, u = i % 16, which = i / 16 / rows;  // whole rows: swizzled or not
           *reinterpret_cast<uint4*>(tile + which * TILE_BYTES + (u / 8) * CHUNK_BYTES + r * 128 + (u % 8) * 16) =

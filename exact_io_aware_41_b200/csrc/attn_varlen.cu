@@ -236,22 +236,25 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// dQ = scale * accumulator, bf16, for the rows that a sequence owns
-__global__ void __launch_bounds__(256)
+// dQ = scale * accumulator, bf16, for the rows that a sequence owns: a warp per packed row, all heads.
+constexpr int kPostThreads = 256;
+__global__ void __launch_bounds__(kPostThreads)
     varlen_bwd_post_kernel(const int* count, const float* acc, const int32_t* row_of, __nv_bfloat16* __restrict__ dq,
                            int Tq, int Hq, float scale) {
   pdl_wait();
   if (*count < 0) return;
-  const int per_row = Hq * (bwd::D / 4);
-  const size_t n4 = size_t(Tq) * per_row;
-  for (size_t i = blockIdx.x * size_t(blockDim.x) + threadIdx.x; i < n4; i += size_t(gridDim.x) * blockDim.x) {
-    const int t = int(i / per_row), e = int(i % per_row), r = row_of[t];
+  const int per_row = Hq * (bwd::D / 4), lane = threadIdx.x & 31;
+  const int n_warps = int(gridDim.x) * (kPostThreads / 32);
+  for (long long t = blockIdx.x * (kPostThreads / 32) + (threadIdx.x >> 5); t < Tq; t += n_warps) {
+    const int r = row_of[t];
     if (r < 0) continue;
-    const float4 v = reinterpret_cast<const float4*>(acc)[size_t(r) * per_row + e];
-    uint2 x;
-    x.x = pack_bf16x2(v.x * scale, v.y * scale);
-    x.y = pack_bf16x2(v.z * scale, v.w * scale);
-    reinterpret_cast<uint2*>(dq)[i] = x;
+    const float4* src = reinterpret_cast<const float4*>(acc) + size_t(r) * per_row;
+    uint2* dst = reinterpret_cast<uint2*>(dq) + size_t(t) * per_row;
+#pragma unroll 4
+    for (int e = lane; e < per_row; e += 32) {
+      const float4 v = src[e];
+      dst[e] = make_uint2(pack_bf16x2(v.x * scale, v.y * scale), pack_bf16x2(v.z * scale, v.w * scale));
+    }
   }
 }
 
@@ -370,13 +373,13 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
   st = bwd_varlen_launch(plan, q, k, v, dout, dk, dv, w.acc, w.acc_rows, w.lse2, w.dd, w.lse_rows, Tq, Tk, Hq, Hkv,
                          q_stride, k_stride, v_stride, scale, causal, stream);
   if (st != ATTN_OK) return st;
-  const size_t n4 = size_t(Tq) * Hq * bwd::D / 4;
+  const long long post = ((long long)Tq + kPostThreads / 32 - 1) / (kPostThreads / 32);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(unsigned(n4 / 256 + 1 < 8192 ? n4 / 256 + 1 : 8192));
-  lc.blockDim = dim3(256);
+  lc.gridDim = dim3(unsigned(post < 16ll * sms ? post : 16ll * sms));
+  lc.blockDim = dim3(kPostThreads);
   lc.stream = stream;
   lc.attrs = at;
   lc.numAttrs = 1;
