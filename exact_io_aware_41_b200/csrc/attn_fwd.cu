@@ -206,11 +206,11 @@ __device__ __forceinline__ Unit unit_at(const FwdArgs& a, int lin) {
 
 // Packed sequences: the units are, for one L2 group of heads after the other, the planned blocks of all sequences
 // (heaviest first; `blocks` of them), every head of the group in turn. The block and head of unit `lin`.
-__device__ __forceinline__ int var_place(const FwdArgs& a, int blocks, int lin, int& h) {
-  const int grp = lin / (a.heads_per_group * blocks);
-  const int r_in = lin - grp * a.heads_per_group * blocks;
-  const int gh = min(a.heads_per_group, a.Hq - grp * a.heads_per_group);  // heads in this group
-  h = grp * a.heads_per_group + r_in % gh;
+__device__ __forceinline__ int var_place(const FwdArgs& a, int blocks, int group_heads, int lin, int& h) {
+  const int grp = lin / (group_heads * blocks);
+  const int r_in = lin - grp * group_heads * blocks;
+  const int gh = min(group_heads, a.Hq - grp * group_heads);  // heads in this group
+  h = grp * group_heads + r_in % gh;
   return r_in / gh;
 }
 
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint64_t T = args.timeout_ns;
-  int total_units = VL ? 0 : args.B * args.Hq * args.n_qblk, var_blocks = 0;
+  int total_units = VL ? 0 : args.B * args.Hq * args.n_qblk, var_blocks = 0, var_heads = 1;
   // CTA pair: rank 0 (the leader) issues the MMAs of both; barriers that the MMAs, the TMA copies
   // of both CTAs or the softmax warps of both CTAs feed live in the leader's shared memory
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   if constexpr (VL) {
     pdl_wait();  // the plan, a kernel of its own, is in memory
     var_blocks = max(0, *args.var_count);
+    var_heads = args.var_count[1];
     total_units = var_blocks * args.Hq;
   }
   // With two softmax warpgroups the 128 control threads give registers to the 256 softmax threads:
@@ -416,10 +417,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
     if constexpr (VL) {
       int h = lin;
       if (PAIR) {
-        e = *reinterpret_cast<const int4*>(args.var_units + var_place(args, var_blocks, lin, h));
+        e = *reinterpret_cast<const int4*>(args.var_units + var_place(args, var_blocks, var_heads, lin, h));
         const int ahead = pair_unit(k + 1);
         int h2;
-        if (ahead >= 0) prefetch_l1(args.var_units + var_place(args, var_blocks, ahead, h2));
+        if (ahead >= 0) prefetch_l1(args.var_units + var_place(args, var_blocks, var_heads, ahead, h2));
       }
       un = unit_var<D, PAIR>(args, h, e);
     } else {
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
           if constexpr (VL) {
             int h = -1;
             int4 e = make_int4(0, 0, 0, 0);
-            if (lin >= 0) e = *reinterpret_cast<const int4*>(args.var_units + var_place(args, var_blocks, lin, h));
+            if (lin >= 0) e = *reinterpret_cast<const int4*>(args.var_units + var_place(args, var_blocks, var_heads, lin, h));
             sched_unit[slot] = h;
             sched_var[slot] = e;
             mbar_arrive(&sched_full[slot]);
@@ -1241,12 +1242,6 @@ static attn_status_t launch_fwd_varlen(const VarPlan& plan, const void* q, const
   a.var_units = plan.units;
   a.var_count = plan.count;
   a.var_claim = plan.claim;
-  // heads per L2 group, as in launch_fwd (the K/V rows of all sequences together), in whole GQA groups: two
-  // causal sequences of 8192 keys with 16 heads (134 MB of K/V) run at 1.1 PFLOP/s in groups, 0.93 without
-  const double kv_head = 2.0 * Tk * D * C::EB;
-  const double fit = (causal && kv_head * Hkv <= kL2OneGroupBytes) ? double(Hkv) : 48.0e6 / kv_head;
-  const int groups = fit >= Hkv ? 1 : fit < 1 ? Hkv : int((Hkv + int(fit) - 1) / int(fit));
-  a.heads_per_group = a.group * ((Hkv + groups - 1) / groups);
   const long long units = plan.max_blocks * Hq;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
@@ -1273,6 +1268,16 @@ static attn_status_t launch_fwd_varlen(const VarPlan& plan, const void* q, const
   lc.stream = stream;
   if (cudaLaunchKernelEx(&lc, kernel, tmQ, tmK, tmV, a) != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
   return ATTN_OK;
+}
+
+int fwd_varlen_ctas(int d) {
+  const int sms = sm_count();
+  return d == 256 ? sms / 2 : sms;
+}
+
+int fwd_varlen_groups(int Tk, int Hkv, int d, int causal) {
+  const double bytes = 2.0 * Tk * Hkv * d * 2;
+  return causal && bytes <= kL2OneGroupBytes ? 1 : int(bytes / 48.0e6) + 1;
 }
 
 attn_status_t fwd_varlen_dispatch(const VarPlan& plan, const void* q, const void* k, const void* v, void* o,

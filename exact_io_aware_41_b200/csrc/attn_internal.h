@@ -48,7 +48,7 @@ struct FwdArgs {
   const float* amax_v;
   // packed sequences (B = 1, Nq and Nkv are the rows of the buffers): the plan in the call's workspace
   const VarUnit* var_units;
-  const int* var_count;        // blocks of query rows listed
+  const int* var_count;        // blocks of query rows listed, and query heads per L2 group
   unsigned int* var_claim;     // next unit (block x query head)
 };
 
@@ -101,10 +101,15 @@ attn_status_t fwd_fp8_dispatch(const void* q8, const void* k8, const void* vt8, 
 // The plan of a packed call, in its workspace (attn_varlen.cu).
 struct VarPlan {
   VarUnit* units;        // [max_blocks]
-  int* count;            // blocks listed (-1: the offsets were out of order, nothing is to be written)
+  int* count;            // blocks listed (-1: the offsets were out of order, nothing is to be written);
+                         // count[1], forward: query heads per L2 group
   unsigned int* claim;   // 0 when the plan is made
   long long max_blocks;
 };
+// CTAs (or CTA pairs) that work on units at once, and the head groups into which the K/V of Tk rows would have to
+// be cut for a group to stay in L2 (as launch_fwd sizes them).
+int fwd_varlen_ctas(int d);
+int fwd_varlen_groups(int Tk, int Hkv, int d, int causal);
 attn_status_t fwd_varlen_dispatch(const VarPlan& plan, const void* q, const void* k, const void* v, void* o,
                                   float* lse, int Tq, int Tk, int Hq, int Hkv, int d, long long qs, long long ks,
                                   long long vs, float scale, int causal, cudaStream_t stream);

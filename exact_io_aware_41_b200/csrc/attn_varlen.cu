@@ -49,14 +49,23 @@ struct PlanBwd {
   }
 };
 
-// The plan, by one block of kPlanThreads threads.
+// The plan, by one block of kPlanThreads threads. Returns the tiles of all blocks (to thread 0) and the most that
+// one block walks at most.
+struct PlanSum {
+  unsigned long long tiles;
+  int longest;
+};
 template <class P>
-__device__ __forceinline__ void make_plan(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S,
-                                          int Tq, int Tk, int causal, const VarPlan& plan) {
+__device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S,
+                                             int Tq, int Tk, int causal, const VarPlan& plan) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- check the offsets, and the largest number of tiles
   __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32], most;
-  if (threadIdx.x == 0) most = 0;
+  __shared__ unsigned long long sum;
+  if (threadIdx.x == 0) {
+    most = 0;
+    sum = 0;
+  }
   bins[threadIdx.x] = 0;
   bool bad = false;
   int mx = 0;
@@ -72,7 +81,7 @@ __device__ __forceinline__ void make_plan(const int32_t* __restrict__ cu_q, cons
       *plan.claim = 0;
       atomicOr(&g_error_word, kErrBadLengthBit);
     }
-    return;
+    return PlanSum{0, 0};
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
   if (lane == 0) atomicMax(&most, mx);
@@ -104,7 +113,15 @@ __device__ __forceinline__ void make_plan(const int32_t* __restrict__ cu_q, cons
       }
     }
   };
-  each_block([&](int, const PlanSeq& q, int i) { atomicAdd(&bins[bin_of(P::tiles(q, i, causal))], 1); });
+  unsigned long long tiles = 0;
+  each_block([&](int, const PlanSeq& q, int i) {
+    const int t = P::tiles(q, i, causal);
+    tiles += t;
+    atomicAdd(&bins[bin_of(t)], 1);
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  if (lane == 0 && tiles) atomicAdd(&sum, tiles);
   __syncthreads();
   // exclusive scan of the bins
   const int mine = bins[threadIdx.x];
@@ -128,14 +145,24 @@ __device__ __forceinline__ void make_plan(const int32_t* __restrict__ cu_q, cons
     const int at = atomicAdd(&bins[bin_of(P::tiles(q, i, causal))], 1);
     if (at < plan.max_blocks) plan.units[at] = P::unit(q, seq, i);
   });
+  return PlanSum{sum, max_tiles};
 }
 static_assert(kPlanBins == kPlanThreads, "one bin per thread");
 
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_plan_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S, int Tq, int Tk,
-                       int causal, VarPlan plan) {
+                       int causal, int Hq, int Hkv, int groups, int ctas, VarPlan plan) {
   pdl_launch();
-  make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+  const PlanSum sum = make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+  // `groups` groups of heads, one after the other, would keep each group's K/V in L2; but every group ends with its
+  // own longest blocks still running, so no more of them than leave each CTA half as much again as the longest
+  // block in every group. Measured: sixteen causal sequences of 4096 with 16 heads 1000 us in 6 groups, 1140 us in
+  // one; 8192 + 5003 + 3001 (this rule: one group) 376 us, 395 us in 4.
+  if (threadIdx.x == 0) {
+    const unsigned long long room = 2 * sum.tiles * Hq / (3ull * ctas * max(1, sum.longest));
+    const int n = max(1, int(min((unsigned long long)min(groups, Hkv), room)));
+    plan.count[1] = Hq / Hkv * ((Hkv + n - 1) / n);
+  }
 }
 
 // Workspace of a plan: count and claim counter, blocks.
@@ -328,8 +355,11 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const
     return ATTN_ERR_WORKSPACE;
   const long long max_blocks = fwd_max_blocks(S, Tq);
   if (max_blocks * Hq > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;  // units are counted in 32 bits
+  const int ctas = fwd_varlen_ctas(d);
+  if (ctas <= 0) return ATTN_ERR_CUDA;
   const VarPlan plan = plan_at(workspace, max_blocks);
-  varlen_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+  varlen_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, cu_k, S, Tq, Tk, causal, Hq, Hkv,
+                                                     fwd_varlen_groups(Tk, Hkv, d, causal), ctas, plan);
   if (cudaPeekAtLastError() != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
   return fwd_varlen_dispatch(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, causal,
                              stream);
