@@ -46,7 +46,7 @@ SIGNATURES = {
     "attn_fwd_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "attn_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "attn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, ctypes.c_size_t, _P]),
-    "attn_fwd_varlen_workspace_bytes": (_Z, [_I, _I]),
+    "attn_fwd_varlen_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "attn_fwd_varlen": (_I, [_P] * 7 + [_I] * 6 + [_L, _L, _L, _F, _I, _P, _Z, _P]),
     "attn_bwd_varlen_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "attn_bwd_varlen": (_I, [_P] * 11 + [_I] * 6 + [_L, _L, _L, _F, _I, _P, _Z, _P]),
@@ -399,8 +399,8 @@ def _offsets_of(cu_q, cu_k, int32, device):
     return S
 
 
-def attn_fwd_varlen_workspace_bytes(S: int, Tq: int) -> int:
-    return int(lib_handle().attn_fwd_varlen_workspace_bytes(S, Tq))
+def attn_fwd_varlen_workspace_bytes(S: int, Tq: int, Tk: int, Hq: int, d: int) -> int:
+    return int(lib_handle().attn_fwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d))
 
 
 def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale: float | None = None, causal: bool = False,
@@ -440,7 +440,7 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale: float | Non
     else:
         _dense("lse", lse, torch.float32, (Hq, Tq), dev)
     if workspace is None:
-        workspace = torch.empty(lib.attn_fwd_varlen_workspace_bytes(S, Tq), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.attn_fwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d), dtype=torch.uint8, device=dev)
     else:
         _space(workspace, dev)
     code = lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),

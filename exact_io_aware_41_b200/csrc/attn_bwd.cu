@@ -876,7 +876,7 @@ attn_status_t bwd_varlen_launch(const VarPlan& plan, const void* q, const void* 
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(unsigned(plan.max_blocks * Hkv));
+  lc.gridDim = dim3(unsigned(plan.max_units * Hkv));
   lc.blockDim = dim3(THREADS);
   lc.dynamicSmemBytes = SMEM_BYTES;
   lc.stream = stream;

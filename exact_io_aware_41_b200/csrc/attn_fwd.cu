@@ -139,7 +139,7 @@ struct FwdCfg {
   static constexpr int SMEM_DATA = NQT * Q_TILE_BYTES + STAGES * KV_TILE_BYTES;
   // Pad small-d configurations so only one CTA (and one 512-column TMEM allocation) fits per SM.
   static constexpr int SMEM_MIN = 120 * 1024;
-  static constexpr int SMEM_BYTES_RAW = 1024 + SMEM_DATA + NBARS * 8 + 16 + SCHED * 4 + 16 + SCHED * 16;
+  static constexpr int SMEM_BYTES_RAW = 1024 + SMEM_DATA + NBARS * 8 + 16 + SCHED * 4 + 16 + SCHED * 24;
   static constexpr int SMEM_BYTES = SMEM_BYTES_RAW > SMEM_MIN ? SMEM_BYTES_RAW : SMEM_MIN;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
@@ -173,7 +173,7 @@ struct Unit {
   int n_tile0;   // K/V tiles the first query tile needs (fewer when the last one is above its diagonal)
   // packed sequences (q0 is a packed row; query rows count from it): queries and keys of the unit's sequence,
   // packed row of its first key
-  int nq, nkv, k_row;
+  int nq, nkv, k_row, part;
 };
 
 template <int D, bool PAIR>
@@ -214,9 +214,22 @@ __device__ __forceinline__ int var_place(const FwdArgs& a, int blocks, int group
   return r_in / gh;
 }
 
-// The unit of head h and the block with plan entry e (q_row, nq, k_row, nkv).
+// A plan entry as the roles pass it on: (q_row, nq, k_row, nkv) and (tiles, part).
+struct VarEntry {
+  int4 at;
+  int2 cut;
+};
+__device__ __forceinline__ VarEntry var_entry(const VarUnit* u) {
+  VarEntry e;
+  e.at = *reinterpret_cast<const int4*>(u);
+  e.cut = *reinterpret_cast<const int2*>(&u->tiles);
+  return e;
+}
+
+// The unit of head h and a plan entry.
 template <int D, bool PAIR>
-__device__ __forceinline__ Unit unit_var(const FwdArgs& a, int h, const int4& e) {
+__device__ __forceinline__ Unit unit_var(const FwdArgs& a, int h, const VarEntry& entry) {
+  const int4& e = entry.at;
   using C = FwdCfg<D, false, PAIR>;
   Unit u;
   u.b = 0;
@@ -233,6 +246,9 @@ __device__ __forceinline__ Unit unit_var(const FwdArgs& a, int h, const int4& e)
     const int end0 = min(u.nkv, min(C::BM, u.nq) + diag);
     u.n_tile0 = end0 > 0 ? (end0 + C::BN - 1) / C::BN : 0;
   }
+  u.n_tiles = min(u.n_tiles, entry.cut.x);
+  u.n_tile0 = min(u.n_tile0, u.n_tiles);
+  u.part = entry.cut.y;
   return u;
 }
 
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(v_clean + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   volatile int* sched_unit = reinterpret_cast<volatile int*>(tmem_holder + 2);  // [SCHED]
-  // packed sequences: the units' entries of the plan, beside sched_unit [SCHED] (16-byte aligned)
+  // packed sequences: the units' entries of the plan, beside sched_unit: [SCHED] int4 (16-byte aligned), [SCHED] int2
   int4* sched_var = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(tmem_holder + 2 + C::SCHED) + 15) & ~uintptr_t(15));
 
   const int warp = threadIdx.x >> 5;
@@ -326,6 +342,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   if constexpr (VL) {
     pdl_wait();  // the plan, a kernel of its own, is in memory
     var_blocks = max(0, *args.var_count);
+    pdl_launch();
     var_heads = args.var_count[1];
     total_units = var_blocks * args.Hq;
   }
@@ -390,34 +407,39 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
   // Every consumer role reads the slot and then arrives once (one thread for the MMA warp, lane 0
   // of each softmax warp after the warp has read it).
   // (packed sequences: its head, and its plan entry in e)
-  auto next_unit = [&](int k, bool whole_warp, int4& e) -> int {
+  auto next_unit = [&](int k, bool whole_warp, VarEntry& e) -> int {
     const int slot = k % C::SCHED;
     const uint32_t ph = uint32_t((k / C::SCHED) & 1);
     bool seen = mbar_wait(&sched_full[slot], ph, abort_flag, T);
     if (whole_warp) seen = __all_sync(0xffffffffu, seen);
     if (!seen) return -1;
     const int lin = sched_unit[slot];
-    if (VL) e = sched_var[slot];
+    if (VL) {
+      e.at = sched_var[slot];
+      e.cut = reinterpret_cast<const int2*>(sched_var + C::SCHED)[slot];
+    }
     if (whole_warp) __syncwarp();
     if (!whole_warp || lane == 0) mbar_arrive(&sched_empty[slot]);
     return lin;
   };
   // A pair's units are fixed instead: cluster p of P takes units p, p + P, p + 2P, ... in issue
-  // order, and every role of both CTAs walks the same list.
+  // order, and every role of both CTAs walks the same list. (Packed sequences, whose units differ more: every
+  // second round in reverse, so that the cluster with a round's longest unit gets the next one's shortest.)
   auto pair_unit = [&](int k) -> int {
-    const long long lin = (long long)(blockIdx.x / 2) + (long long)k * (gridDim.x / 2);
+    const int n_pairs = gridDim.x / 2, p = blockIdx.x / 2;
+    const long long lin = (long long)(VL && (k & 1) ? n_pairs - 1 - p : p) + (long long)k * n_pairs;
     return lin < total_units ? int(lin) : -1;
   };
   // The k-th unit of a consumer role; false: no more. A pair's roles read the plan entries themselves, and fetch
   // the next one's line ahead.
   auto take_unit = [&](int k, bool whole_warp, Unit& un) -> bool {
-    int4 e = make_int4(0, 0, 0, 0);
+    VarEntry e = {};
     const int lin = PAIR ? pair_unit(k) : next_unit(k, whole_warp, e);
     if (lin < 0) return false;
     if constexpr (VL) {
       int h = lin;
       if (PAIR) {
-        e = *reinterpret_cast<const int4*>(args.var_units + var_place(args, var_blocks, var_heads, lin, h));
+        e = var_entry(args.var_units + var_place(args, var_blocks, var_heads, lin, h));
         const int ahead = pair_unit(k + 1);
         int h2;
         if (ahead >= 0) prefetch_l1(args.var_units + var_place(args, var_blocks, var_heads, ahead, h2));
@@ -462,10 +484,11 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
           const int lin = claimed < unsigned(total_units) ? int(claimed) : -1;
           if constexpr (VL) {
             int h = -1;
-            int4 e = make_int4(0, 0, 0, 0);
-            if (lin >= 0) e = *reinterpret_cast<const int4*>(args.var_units + var_place(args, var_blocks, var_heads, lin, h));
+            VarEntry e = {};
+            if (lin >= 0) e = var_entry(args.var_units + var_place(args, var_blocks, var_heads, lin, h));
             sched_unit[slot] = h;
-            sched_var[slot] = e;
+            sched_var[slot] = e.at;
+            reinterpret_cast<int2*>(sched_var + C::SCHED)[slot] = e.cut;
             mbar_arrive(&sched_full[slot]);
             un = unit_var<D, PAIR>(args, h, e);
           } else {
@@ -1014,6 +1037,36 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
 
       // ---- epilogue: O = acc / l (once), LSE = scale * m_ref + ln l -------------------------------
       const bool valid = q_row < nq;
+      if (VL && un.part >= 0) {
+        // one part of the block's keys: O / l in fp32 and the part's LSE, joined with the others by a later kernel
+        // (which takes nothing of a part whose LSE is -inf)
+        const size_t slot = (size_t(un.part) * args.Hq + un.h) * C::UNIT_ROWS + q_row;
+        if (my_tiles > 0) {
+          if (!wait_warp(&o_final[qt], uint32_t(uc & 1))) {
+            ok = false;
+            break;
+          }
+          ++uc;
+          tc_fence_after();
+          const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(lane_addr + o_col + cc * 32, o);
+            tmem_ld_wait();
+            tmem_reg_fence32(o);
+            if (valid) {
+              float4* dst = reinterpret_cast<float4*>(args.var_part_o + slot * D + cc * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                     __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+            }
+          }
+        }
+        if (valid) args.var_part_lse[slot] = l != 0.f ? fmaf(m_ref, sc_nat, logf(l)) : -INFINITY;
+        continue;
+      }
       const int out_row = VL ? un.q0 + q_row : q_row;
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(args.o) +
                             ((size_t(un.b) * args.Nq + (valid ? out_row : 0)) * args.Hq + un.h) * D;
@@ -1031,7 +1084,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
         }
         ++uc;
         tc_fence_after();
-        const float inv = (l > 0.f) ? o_mul / l : 0.f;
+        const float inv = (VL ? l != 0.f : l > 0.f) ? o_mul / l : 0.f;
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
@@ -1069,7 +1122,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
       }
       if (valid)
         args.lse[(size_t(un.b) * args.Hq + un.h) * args.Nq + out_row] =
-            (l > 0.f) ? fmaf(m_ref, sc_nat, logf(l)) : -INFINITY;
+            (VL ? l != 0.f : l > 0.f) ? fmaf(m_ref, sc_nat, logf(l)) : -INFINITY;
     }
   }
 
@@ -1210,7 +1263,7 @@ static attn_status_t launch_fwd(const void* q, const void* k, const void* v, voi
 }
 
 // Packed sequences: the plan (`plan`, made by an earlier kernel of the stream) names the units; the launch is
-// programmatic, so that set-up overlaps the plan kernel. max_blocks bounds the planned blocks.
+// programmatic, so that set-up overlaps the plan kernel. max_units bounds the planned units.
 template <int D, bool PAIR>
 static attn_status_t launch_fwd_varlen(const VarPlan& plan, const void* q, const void* k, const void* v, void* o,
                                        float* lse, int Tq, int Tk, int Hq, int Hkv, long long qs, long long ks,
@@ -1242,7 +1295,9 @@ static attn_status_t launch_fwd_varlen(const VarPlan& plan, const void* q, const
   a.var_units = plan.units;
   a.var_count = plan.count;
   a.var_claim = plan.claim;
-  const long long units = plan.max_blocks * Hq;
+  a.var_part_o = plan.part_o;
+  a.var_part_lse = plan.part_lse;
+  const long long units = plan.max_units * Hq;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   long long ctas = units < sms ? units : sms;
@@ -1271,7 +1326,8 @@ static attn_status_t launch_fwd_varlen(const VarPlan& plan, const void* q, const
 }
 
 int fwd_varlen_ctas(int d) {
-  const int sms = sm_count();
+  int sms = sm_count();
+  if (sms <= 0) sms = 148;  // no device visible: size for a B200
   return d == 256 ? sms / 2 : sms;
 }
 

@@ -21,14 +21,23 @@ enum : unsigned int {
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
 // Packed sequences: one block of one sequence, as the plan lists them. Forward: a block of query rows, q_row and nq
-// from its first row on. Backward: a block of keys, k_row and nkv from its first key on.
+// from its first row on; where the plan cuts its keys into parts, one part of them, k_row and nkv from the part's
+// first key on. Backward: a block of keys, k_row and nkv from its first key on.
 struct __align__(16) VarUnit {
   int q_row;  // packed row of the first query
   int nq;     // the sequence's queries from that row on
   int k_row;  // packed row of the first key
   int nkv;    // the sequence's keys from that row on
-  int seq;
-  int pad[3];
+  int tiles;  // forward: key tiles of the part (at most)
+  int part;   // forward: slot of the part's result (-1: the block is whole)
+  int seq;    // backward
+  int pad;
+};
+
+// A block of query rows whose parts are to be joined.
+struct __align__(16) VarJoin {
+  int q_row, rows;
+  int part, parts;  // first slot, and how many
 };
 
 struct FwdArgs {
@@ -50,6 +59,8 @@ struct FwdArgs {
   const VarUnit* var_units;
   const int* var_count;        // blocks of query rows listed, and query heads per L2 group
   unsigned int* var_claim;     // next unit (block x query head)
+  float* var_part_o;           // [slot][Hq][256][d]: parts, each normalised by its own sum
+  float* var_part_lse;         // [slot][Hq][256]
 };
 
 bool is_aligned16(const void* p);
@@ -100,11 +111,16 @@ attn_status_t fwd_fp8_dispatch(const void* q8, const void* k8, const void* vt8, 
 
 // The plan of a packed call, in its workspace (attn_varlen.cu).
 struct VarPlan {
-  VarUnit* units;        // [max_blocks]
-  int* count;            // blocks listed (-1: the offsets were out of order, nothing is to be written);
-                         // count[1], forward: query heads per L2 group
+  VarUnit* units;        // [max_units]
+  int* count;            // units listed (-1: the offsets were out of order, nothing is to be written);
+                         // forward: count[1] query heads per L2 group, count[2] joins
   unsigned int* claim;   // 0 when the plan is made
-  long long max_blocks;
+  long long max_units;
+  // forward, where keys may be cut into parts (max_parts > 0)
+  VarJoin* joins;        // [max_parts]
+  float* part_o;
+  float* part_lse;
+  int max_parts;
 };
 // CTAs (or CTA pairs) that work on units at once, and the head groups into which the K/V of Tk rows would have to
 // be cut for a group to stay in L2 (as launch_fwd sizes them).

@@ -33,8 +33,10 @@ struct PlanFwd {
     const int end = causal ? min(s.nkv, min(kFwdBlockRows, left) + s.nkv - left) : s.nkv;
     return end > 0 ? (end + kTileRows - 1) / kTileRows : 0;
   }
-  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk) {
-    return VarUnit{s.q0 + blk * kFwdBlockRows, s.nq - blk * kFwdBlockRows, s.k0, s.nkv, seq, {0, 0, 0}};
+  // tiles [lo, hi) of the block's, as part `part` (-1: all of them)
+  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int, int blk, int lo, int hi, int part) {
+    return VarUnit{s.q0 + blk * kFwdBlockRows, s.nq - blk * kFwdBlockRows, s.k0 + lo * kTileRows,
+                   s.nkv - lo * kTileRows,     hi - lo,                    part, 0, 0};
   }
 };
 // Backward: blocks of 128 keys, and the tiles of 128 query rows that block `blk` walks.
@@ -44,40 +46,60 @@ struct PlanBwd {
   static __device__ __forceinline__ int tiles(const PlanSeq& s, int blk, int causal) {
     return max(0, longest(s) - first_q_tile(causal, s.nq, s.nkv - blk * kTileRows));
   }
-  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk) {
-    return VarUnit{s.q0, s.nq, s.k0 + blk * kTileRows, s.nkv - blk * kTileRows, seq, {0, 0, 0}};
+  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk, int, int, int) {
+    return VarUnit{s.q0, s.nq, s.k0 + blk * kTileRows, s.nkv - blk * kTileRows, 0, -1, seq, 0};
   }
 };
 
+// Tiles of a part, at least: below that a part's own cost (its queries, the partial result, the join) outweighs what
+// is gained (measured with 4, 8 and 16).
+constexpr int kMinPartTiles = 8;
+
+// First tile of the k-th of n parts of t tiles (t below 2^24, n below 256).
+__device__ __forceinline__ int cut_at(int k, int t, int n) { return int(unsigned(k) * unsigned(t) / unsigned(n)); }
+
 // The plan, by one block of kPlanThreads threads. Returns the tiles of all blocks (to thread 0) and the most that
 // one block walks at most.
+//
+// share > 0 (forward, few blocks): a block is cut into parts of about max(kMinPartTiles, share-th of all tiles) by
+// rounding, where that gives two or more. With x = its tiles / that size such a block has at most 4 x / 3 parts and
+// x - 1/2 of them beyond the first, and the x sum to at most `share`: so at most 4 share / 3 parts are joined, and
+// at most `share` units are listed beyond one per block.
 struct PlanSum {
   unsigned long long tiles;
   int longest;
 };
 template <class P>
 __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S,
-                                             int Tq, int Tk, int causal, const VarPlan& plan) {
+                                             int Tq, int Tk, int causal, int share, const VarPlan& plan) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- check the offsets, and the largest number of tiles
   __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32], most;
   __shared__ unsigned long long sum;
+  __shared__ int parts_given, joins_given;
   if (threadIdx.x == 0) {
     most = 0;
     sum = 0;
+    parts_given = 0;
+    joins_given = 0;
   }
   bins[threadIdx.x] = 0;
   bool bad = false;
   int mx = 0;
-  for (int s = threadIdx.x; s < S; s += kPlanThreads) {
+  auto load = [&](int s) -> PlanSeq {
+    if (s >= S) return PlanSeq{0, 0, 0, 0};
     const int a = cu_q[s], b = cu_q[s + 1], c = cu_k[s], e = cu_k[s + 1];
     bad |= a < 0 || b < a || b > Tq || c < 0 || e < c || e > Tk;
-    mx = max(mx, P::longest(PlanSeq{a, b - a, c, e - c}));
-  }
+    return PlanSeq{a, b - a, c, e - c};
+  };
+  const PlanSeq own = load(threadIdx.x);  // this thread's first sequence, kept for the passes below
+  mx = P::longest(own);
+  for (int s = threadIdx.x + kPlanThreads; s < S; s += kPlanThreads) mx = max(mx, P::longest(load(s)));
   bad = __syncthreads_or(bad);
   if (bad) {
     if (threadIdx.x == 0) {
       *plan.count = -1;
+      plan.count[2] = 0;
       *plan.claim = 0;
       atomicOr(&g_error_word, kErrBadLengthBit);
     }
@@ -94,13 +116,7 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   auto each_block = [&](auto f) {
     for (int s0 = warp * 32; s0 < S; s0 += kPlanThreads) {
       const int s = s0 + lane;
-      PlanSeq q = {0, 0, 0, 0};
-      if (s < S) {
-        q.q0 = cu_q[s];
-        q.nq = cu_q[s + 1] - q.q0;
-        q.k0 = cu_k[s];
-        q.nkv = cu_k[s + 1] - q.k0;
-      }
+      const PlanSeq q = s < kPlanThreads ? own : load(s);
       const int nb = P::blocks(q);
       if (nb <= kPlanOwnBlocks)
         for (int i = 0; i < nb; ++i) f(s, q, i);
@@ -117,12 +133,21 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   each_block([&](int, const PlanSeq& q, int i) {
     const int t = P::tiles(q, i, causal);
     tiles += t;
-    atomicAdd(&bins[bin_of(t)], 1);
+    if (share == 0) atomicAdd(&bins[bin_of(t)], 1);
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   if (lane == 0 && tiles) atomicAdd(&sum, tiles);
   __syncthreads();
+  int part_tiles = 0x7FFFFFFF;
+  if (share > 0) {
+    part_tiles = int(min(0x3FFFFFFFull, max((unsigned long long)kMinPartTiles, (sum + share - 1) / share)));
+    each_block([&](int, const PlanSeq& q, int i) {
+      const int t = P::tiles(q, i, causal), n = max(1, (t + part_tiles / 2) / part_tiles);
+      for (int k = 0; k < n; ++k) atomicAdd(&bins[bin_of(cut_at(k + 1, t, n) - cut_at(k, t, n))], 1);
+    });
+    __syncthreads();
+  }
   // exclusive scan of the bins
   const int mine = bins[threadIdx.x];
   int scan = mine;
@@ -133,27 +158,46 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   }
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
-  int before = scan - mine;
-  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  int before = warp_sum[lane];  // (kPlanThreads / 32 == 32 warps)
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  before = __shfl_sync(0xffffffffu, before, warp) - warp_sum[warp] + scan - mine;
   bins[threadIdx.x] = before;
   if (threadIdx.x == kPlanThreads - 1) {
-    *plan.count = int(min((long long)(before + mine), plan.max_blocks));
+    *plan.count = int(min((long long)(before + mine), plan.max_units));
     *plan.claim = 0;
   }
   __syncthreads();
   each_block([&](int seq, const PlanSeq& q, int i) {
-    const int at = atomicAdd(&bins[bin_of(P::tiles(q, i, causal))], 1);
-    if (at < plan.max_blocks) plan.units[at] = P::unit(q, seq, i);
+    const int t = P::tiles(q, i, causal), n = share > 0 ? max(1, (t + part_tiles / 2) / part_tiles) : 1;
+    int part = -1;
+    if (n > 1) {
+      part = atomicAdd(&parts_given, n);
+      if (part + n > plan.max_parts) return;  // (cannot be: see above)
+      const PlanSeq& s = q;
+      plan.joins[atomicAdd(&joins_given, 1)] =
+          VarJoin{s.q0 + i * kFwdBlockRows, min(kFwdBlockRows, s.nq - i * kFwdBlockRows), part, n};
+    }
+    for (int k = 0; k < n; ++k) {
+      const int lo = cut_at(k, t, n), hi = cut_at(k + 1, t, n);
+      const int at = atomicAdd(&bins[bin_of(hi - lo)], 1);
+      if (at < plan.max_units) plan.units[at] = P::unit(q, seq, i, lo, n > 1 ? hi : t, n > 1 ? part + k : -1);
+    }
   });
+  __syncthreads();
+  if (threadIdx.x == 0) plan.count[2] = joins_given;
   return PlanSum{sum, max_tiles};
 }
-static_assert(kPlanBins == kPlanThreads, "one bin per thread");
+static_assert(kPlanBins == kPlanThreads && kPlanThreads == 1024, "one bin per thread, one warp sum per lane");
 
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_plan_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S, int Tq, int Tk,
-                       int causal, int Hq, int Hkv, int groups, int ctas, VarPlan plan) {
+                       int causal, int Hq, int Hkv, int groups, int ctas, int share, VarPlan plan) {
   pdl_launch();
-  const PlanSum sum = make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+  const PlanSum sum = make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, share, plan);
   // `groups` groups of heads, one after the other, would keep each group's K/V in L2; but every group ends with its
   // own longest blocks still running, so no more of them than leave each CTA half as much again as the longest
   // block in every group. Measured: sixteen causal sequences of 4096 with 16 heads 1000 us in 6 groups, 1140 us in
@@ -165,19 +209,116 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// Workspace of a plan: count and claim counter, blocks.
+// Joins the parts of the query blocks whose keys were cut: a warp per row and head, LSE = log sum_s exp(lse_s),
+// O = sum_s exp(lse_s - LSE) o_s over the parts in order; parts with lse_s = -inf are not read. Bound by memory: fp32
+// parts of 256 rows are read once, mostly from L2.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    varlen_join_kernel(const int* count, const VarJoin* joins, const float* part_o, const float* part_lse,
+                       __nv_bfloat16* __restrict__ o, float* __restrict__ lse, int Tq, int Hq) {
+  constexpr int EPL = D / 32;  // consecutive elements of d per lane
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)count[2] * Hq * kFwdBlockRows;
+  const long long step = (long long)gridDim.x * kJoinWarps;
+  for (long long w = blockIdx.x * (long long)kJoinWarps + (threadIdx.x >> 5); w < rows; w += step) {
+    const int r = int(w % kFwdBlockRows), h = int(w / kFwdBlockRows % Hq);
+    const VarJoin j = joins[w / kFwdBlockRows / Hq];
+    if (r >= j.rows) continue;
+    auto slot = [&](int s) -> size_t { return (size_t(j.part + s) * Hq + h) * kFwdBlockRows + r; };
+    float mx = -INFINITY;
+    for (int s = lane; s < j.parts; s += 32) mx = fmaxf(mx, part_lse[slot(s)]);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float z = 0.f, acc[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    for (int s = 0; s < j.parts; ++s) {
+      const float l = part_lse[slot(s)];
+      if (l == -INFINITY) continue;
+      const float f = expf(l - ref);
+      z += f;
+      const float* src = part_o + slot(s) * D + lane * EPL;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+    }
+    const float inv = z != 0.f ? 1.f / z : 0.f;
+    __nv_bfloat16* dst = o + (size_t(j.q_row + r) * Hq + h) * D + lane * EPL;
+    if constexpr (EPL == 1) {
+      dst[0] = __float2bfloat16_rn(acc[0] * inv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPL; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+    if (lane == 0) lse[size_t(h) * Tq + j.q_row + r] = z != 0.f ? mx + logf(z) : -INFINITY;
+  }
+}
+
+template <int D>
+attn_status_t launch_join(const VarPlan& plan, void* o, float* lse, int Tq, int Hq, int sms, cudaStream_t stream) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(unsigned(8 * sms));
+  lc.blockDim = dim3(kJoinWarps * 32);
+  lc.stream = stream;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, varlen_join_kernel<D>, static_cast<const int*>(plan.count),
+                         static_cast<const VarJoin*>(plan.joins), static_cast<const float*>(plan.part_o),
+                         static_cast<const float*>(plan.part_lse), static_cast<__nv_bfloat16*>(o), lse, Tq,
+                         Hq) != cudaSuccess)
+    return cudaGetLastError(), ATTN_ERR_CUDA;
+  return ATTN_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace of a plan: counts and claim counter, units.
 long long fwd_max_blocks(int S, int Tq) { return (long long)Tq / kFwdBlockRows + S; }
 long long bwd_max_blocks(int S, int Tk) { return (long long)Tk / kTileRows + S; }
-size_t plan_bytes(long long max_blocks) { return 256 + (size_t(max_blocks) * sizeof(VarUnit) + 255) / 256 * 256; }
+size_t plan_bytes(long long max_units) { return 256 + up256(size_t(max_units) * sizeof(VarUnit)); }
 
-VarPlan plan_at(void* workspace, long long max_blocks) {
+VarPlan plan_at(void* workspace, long long max_units) {
   char* w = static_cast<char*>(workspace);
-  VarPlan p;
+  VarPlan p = {};
   p.count = reinterpret_cast<int*>(w);
   p.claim = reinterpret_cast<unsigned int*>(w + 128);
   p.units = reinterpret_cast<VarUnit*>(w + 256);
-  p.max_blocks = max_blocks;
+  p.max_units = max_units;
   return p;
+}
+
+// Forward: into how many shares the tiles are cut for blocks to be cut into parts of a share's size; 0: no block is
+// cut. Keys are cut where there are too few blocks to keep the CTAs busy and enough keys that one could be long: the
+// parts cost up to 39 MB of workspace and a kernel to join them, which many blocks, or short ones, do not pay back.
+int fwd_share(int S, int Tq, int Tk, int Hq, int d) {
+  const int ctas = fwd_varlen_ctas(d);
+  if (Tk < 2 * kMinPartTiles * kTileRows || fwd_max_blocks(S, Tq) * Hq > 4ll * ctas) return 0;
+  return ctas / Hq;
+}
+
+// The forward workspace: its size, and where its parts are (workspace may be null).
+size_t fwd_space(void* workspace, int S, int Tq, int Tk, int Hq, int d, int share, VarPlan* plan) {
+  const long long max_units = fwd_max_blocks(S, Tq) + share;
+  *plan = plan_at(workspace, max_units);
+  size_t n = plan_bytes(max_units);
+  if (share > 0) {
+    plan->max_parts = 4 * share / 3 + 1;
+    char* w = static_cast<char*>(workspace);
+    plan->joins = reinterpret_cast<VarJoin*>(w + n);
+    n += up256(plan->max_parts * sizeof(VarJoin));
+    const size_t rows = size_t(plan->max_parts) * Hq * kFwdBlockRows;
+    plan->part_lse = reinterpret_cast<float*>(w + n);
+    n += up256(rows * sizeof(float));
+    plan->part_o = reinterpret_cast<float*>(w + n);
+    n += up256(rows * d * sizeof(float));
+  }
+  return n;
 }
 
 // The sequence that owns packed row t (-1: none): the last s with cu[s] <= t, if t < cu[s + 1].
@@ -217,7 +358,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                           BwdSpace w) {
   pdl_launch();
   if (blockIdx.x == 0) {
-    make_plan<PlanBwd>(cu_q, cu_k, S, Tq, Tk, causal, plan);
+    make_plan<PlanBwd>(cu_q, cu_k, S, Tq, Tk, causal, 0, plan);
     return;
   }
   const int lane = threadIdx.x & 31, seg = lane & 15;
@@ -285,8 +426,6 @@ __global__ void __launch_bounds__(kPostThreads)
   }
 }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-
 // The backward workspace: its size (workspace null), or where its parts are.
 size_t bwd_space(void* workspace, int S, int Tq, int Tk, int Hq, VarPlan* plan, BwdSpace* w) {
   const long long max_blocks = bwd_max_blocks(S, Tk);
@@ -337,9 +476,10 @@ using namespace attn;
 
 extern "C" {
 
-size_t attn_fwd_varlen_workspace_bytes(int S, int Tq) {
-  if (S < 1 || Tq < 1 || S > kVarMaxSeqs) return 0;
-  return plan_bytes(fwd_max_blocks(S, Tq));
+size_t attn_fwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d) {
+  if (S < 1 || Tq < 1 || Tk < 1 || Hq < 1 || d < 1 || S > kVarMaxSeqs) return 0;
+  VarPlan plan;
+  return fwd_space(nullptr, S, Tq, Tk, Hq, d, fwd_share(S, Tq, Tk, Hq, d), &plan);
 }
 
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const int32_t* cu_q, const int32_t* cu_k,
@@ -350,19 +490,27 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const
   attn_status_t st =
       varlen_args_status(ptrs, 4, lse, cu_q, cu_k, S, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, causal);
   if (st != ATTN_OK) return st;
+  const int share = fwd_share(S, Tq, Tk, Hq, d);
+  VarPlan plan;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      workspace_bytes < attn_fwd_varlen_workspace_bytes(S, Tq))
+      workspace_bytes < fwd_space(workspace, S, Tq, Tk, Hq, d, share, &plan))
     return ATTN_ERR_WORKSPACE;
-  const long long max_blocks = fwd_max_blocks(S, Tq);
-  if (max_blocks * Hq > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;  // units are counted in 32 bits
-  const int ctas = fwd_varlen_ctas(d);
-  if (ctas <= 0) return ATTN_ERR_CUDA;
-  const VarPlan plan = plan_at(workspace, max_blocks);
+  if (plan.max_units * Hq > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;  // units are counted in 32 bits
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
   varlen_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, cu_k, S, Tq, Tk, causal, Hq, Hkv,
-                                                     fwd_varlen_groups(Tk, Hkv, d, causal), ctas, plan);
+                                                     fwd_varlen_groups(Tk, Hkv, d, causal), fwd_varlen_ctas(d), share,
+                                                     plan);
   if (cudaPeekAtLastError() != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
-  return fwd_varlen_dispatch(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, causal,
-                             stream);
+  st = fwd_varlen_dispatch(plan, q, k, v, o, lse, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, causal,
+                           stream);
+  if (st != ATTN_OK || share == 0) return st;
+  switch (d) {
+    case 32: return launch_join<32>(plan, o, lse, Tq, Hq, sms, stream);
+    case 64: return launch_join<64>(plan, o, lse, Tq, Hq, sms, stream);
+    case 128: return launch_join<128>(plan, o, lse, Tq, Hq, sms, stream);
+    default: return launch_join<256>(plan, o, lse, Tq, Hq, sms, stream);
+  }
 }
 
 size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d) {
@@ -389,7 +537,7 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
   BwdSpace w;
   bwd_space(workspace, S, Tq, Tk, Hq, &plan, &w);
   // tile coordinates, and the grid, are 32-bit
-  if (plan.max_blocks * Hkv > 0x7FFFFFFFll || w.acc_rows > 0x7FFFFFFFll || w.lse_rows > 0x7FFFFFFFll)
+  if (plan.max_units * Hkv > 0x7FFFFFFFll || w.acc_rows > 0x7FFFFFFFll || w.lse_rows > 0x7FFFFFFFll)
     return ATTN_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;

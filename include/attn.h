@@ -218,7 +218,7 @@ attn_status_t attn_decode_combine(const float* part_o, const float* part_lse, in
  *   o    [Tq, Hq, d] bf16, dense, written;  lse [Hq, Tq] fp32, written
  *   causal = 1: query i of a sequence sees its key j iff j <= i + Nkv - Nq, with the sequence's own
  *        lengths. A query that sees no key (an empty key range included) gets O = 0 and LSE = -inf.
- *   workspace   at least attn_fwd_varlen_workspace_bytes(S, Tq) bytes, 256-byte aligned, no
+ *   workspace   at least attn_fwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d) bytes, 256-byte aligned, no
  *        initialisation needed. Calls that may overlap on the GPU need workspaces of their own.
  *   S, Tq, Tk, Hq, Hkv >= 1, S <= 1000000, d in {32, 64, 128, 256}; scale as attn_fwd.
  * Rows of q that no sequence owns (before cu_q[0], from cu_q[S] on) are not read by any sequence's result
@@ -226,7 +226,7 @@ attn_status_t attn_decode_combine(const float* part_o, const float* part_lse, in
  * included, never reaches a sequence's result. Offsets that break the order above set the device error
  * word (ATTN_ERR_INVALID_ARG from attn_get_last_error) and nothing at all is written.
  */
-size_t attn_fwd_varlen_workspace_bytes(int S, int Tq);
+size_t attn_fwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d);
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const int32_t* cu_q, const int32_t* cu_k,
                               void* o, float* lse, int S, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride,
                               long long k_stride, long long v_stride, float scale, int causal, void* workspace,

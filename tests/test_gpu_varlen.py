@@ -75,6 +75,54 @@ def test_forward_many_short_sequences(lib, d):
     _check_forward(lib, 7300 + d, lens, lens, 2, 1, d, True)
 
 
+CUT = [
+    ([40, 300], [9000, 4500], 2, 1),            # two blocks with many keys: each cut into parts
+    ([1], [20011], 1, 1),                       # one query: as many parts as there are shares
+    ([512, 3, 256], [2600, 129, 6000], 4, 2),   # whole blocks and cut ones together
+    ([2000], [2100], 3, 1),                     # causal: early blocks short, late ones cut
+    ([700], [5000], 16, 4),
+]
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("case", range(len(CUT)))
+def test_forward_keys_cut_into_parts(lib, d, causal, case):
+    ql, kl, Hq, Hkv = CUT[case]
+    _check_forward(lib, 7350 + 10 * case + d + int(causal), ql, kl, Hq, Hkv, d, causal)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_parts_do_not_take_rows_of_others(lib, d):
+    """Blocks cut into parts beside sequences of NaN, and rows that see keys of the last part only (more queries
+    than keys would give none): finite results, the rows of nobody left as they were."""
+    import torch
+
+    ql, kl, Hq, Hkv, pad = [130, 64], [5000, 3003], 2, 1, 3
+    qb, kb, vb = draw_packed(7390 + d, ql, kl, Hq, Hkv, d)
+
+    def surrounded(bits, heads):
+        t = torch.full((bits.shape[0] + 2 * pad, heads, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        t[pad:-pad] = gpu(bits)
+        return t
+
+    q, k, v = surrounded(qb, Hq), surrounded(kb, Hkv), surrounded(vb, Hkv)
+    k[pad:pad + kl[0]], v[pad:pad + kl[0]] = float("nan"), float("inf")  # the first sequence: NaN throughout
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((Hq, q.shape[0]), 7.0, device="cuda")
+    lib.attn_fwd_varlen(q, k, v, offsets(ql, pad), offsets(kl, pad), causal=True, out=o, lse=lse)
+    sc = 1 / math.sqrt(d)
+    a, b = list(sequences(ql, kl))[1]
+    O, L, bO, bL = reference(f64(qb)[a], f64(kb)[b], f64(vb)[b], [64], [3003], sc, True)
+    own = slice(pad + a.start, pad + a.stop)
+    assert_within(host(o[own].contiguous()), O, bO, "beside NaN")
+    assert_lse(lse[:, own].cpu().numpy().astype(np.float64), L, bL, "beside NaN")
+    for x in (o[:pad], o[-pad:], lse[:, :pad], lse[:, -pad:]):
+        assert bool((x == 7.0).all())
+    assert bool(torch.isnan(o[pad:pad + 130].float()).all())  # NaN keys give NaN, not a number
+    assert lib.attn_get_last_error() == lib.ATTN_OK
+
+
 def test_forward_large_scores_and_groups(lib):
     _check_forward(lib, 7400, [260, 70], [260, 70], 16, 1, 128, True, scale=2.0)
 
@@ -244,7 +292,7 @@ def test_graph_replays_with_new_offsets(lib):
     T, Hq, Hkv, d = 600, 4, 2, 128
     q, k, v, do = (torch.empty((T, h, d), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv, Hq))
     cu = offsets([200, 200, 200])
-    ws = torch.empty(lib.attn_fwd_varlen_workspace_bytes(3, T), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(lib.attn_fwd_varlen_workspace_bytes(3, T, T, Hq, d), dtype=torch.uint8, device="cuda")
     ws_b = torch.empty(lib.attn_bwd_varlen_workspace_bytes(3, T, T, Hq, d), dtype=torch.uint8, device="cuda")
     o, lse = torch.empty_like(q), torch.empty((Hq, T), device="cuda")
     g = [torch.empty_like(t) for t in (q, k, v)]

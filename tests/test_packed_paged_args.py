@@ -35,7 +35,7 @@ def test_packed_forward_refusals(c):
         assert call(**bad) == pkg.ATTN_ERR_INVALID_ARG, bad
     assert call(d=48) == pkg.ATTN_ERR_UNSUPPORTED
     assert call(S=1000001) == pkg.ATTN_ERR_UNSUPPORTED
-    need = lib.attn_fwd_varlen_workspace_bytes(2, 16)
+    need = lib.attn_fwd_varlen_workspace_bytes(2, 16, 16, 4, 64)
     for bad in (dict(ws=0), dict(ws=P + 16), dict(n=need - 1)):
         assert call(**bad) == pkg.ATTN_ERR_WORKSPACE, bad
 
@@ -106,10 +106,14 @@ def test_cache_append_refusals(c):
 
 def test_workspace_sizes(c):
     pkg, _ = c
-    assert pkg.attn_fwd_varlen_workspace_bytes(0, 16) == 0 and pkg.attn_fwd_varlen_workspace_bytes(3, 0) == 0
+    assert pkg.attn_fwd_varlen_workspace_bytes(0, 16, 16, 4, 64) == 0
+    assert pkg.attn_fwd_varlen_workspace_bytes(3, 0, 16, 4, 64) == 0
     assert pkg.attn_bwd_varlen_workspace_bytes(1, 0, 1, 1, 128) == 0
     assert pkg.attn_decode_paged_workspace_bytes(2, 3, 2, 64) == 0
-    assert pkg.attn_fwd_varlen_workspace_bytes(3, 1000) <= pkg.attn_fwd_varlen_workspace_bytes(300, 1000)
+    # a list of 3 + 300 blocks of 32 bytes (and the counters); room for parts only with few blocks and many keys
+    assert pkg.attn_fwd_varlen_workspace_bytes(300, 1000, 1000, 8, 64) == 256 + 256 * math.ceil(303 * 32 / 256)
+    assert pkg.attn_fwd_varlen_workspace_bytes(3, 100000, 100000, 8, 64) < 1 << 20
+    assert 1 << 20 < pkg.attn_fwd_varlen_workspace_bytes(3, 1000, 100000, 8, 64) < 41 << 20
 
 
 def test_binding_refusals():
