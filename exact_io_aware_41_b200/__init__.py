@@ -48,7 +48,7 @@ SIGNATURES = {
     "attn_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, ctypes.c_size_t, _P]),
     "attn_fwd_varlen_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "attn_fwd_varlen": (_I, [_P] * 7 + [_I] * 6 + [_L, _L, _L, _F, _I, _P, _Z, _P]),
-    "attn_bwd_varlen_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "attn_bwd_varlen_workspace_bytes": (_Z, [_I] * 6),
     "attn_bwd_varlen": (_I, [_P] * 11 + [_I] * 6 + [_L, _L, _L, _F, _I, _P, _Z, _P]),
     "attn_decode_paged_workspace_bytes": (_Z, [_I, _I, _I, _I]),
     "attn_decode_paged": (_I, [_P] * 5 + [_I, _I, _I, _P, _P, _I, _I, _I, _I, _L, _F, _P, _Z, _P]),
@@ -451,8 +451,8 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale: float | Non
     return out, lse
 
 
-def attn_bwd_varlen_workspace_bytes(S: int, Tq: int, Tk: int, Hq: int, d: int) -> int:
-    return int(lib_handle().attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d))
+def attn_bwd_varlen_workspace_bytes(S: int, Tq: int, Tk: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib_handle().attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, Hkv, d))
 
 
 def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k=None, scale: float | None = None,
@@ -495,7 +495,8 @@ def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k=None, scal
     else:
         _dense("dv", dv, bf16, k.shape, dev)
     if workspace is None:
-        workspace = torch.empty(lib.attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, Hkv, d), dtype=torch.uint8,
+                                device=dev)
     else:
         _space(workspace, dev)
     code = lib.attn_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),

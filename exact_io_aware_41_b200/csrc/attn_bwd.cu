@@ -90,6 +90,7 @@ struct BwdArgs {
   // rows): the planned key blocks, in the call's workspace
   const VarUnit* var_units;
   const int* var_count;
+  float* var_part_kv;     // parts of a block's dK and dV, fp32: [slot][Hkv][2][128][128]
 };
 
 // Packed sequences: where a sequence's rows start in the padded arrays of the workspace. Every sequence starts at
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
   const int kb = blockIdx.x / per_kb;
   const int b = VL ? 0 : (blockIdx.x % per_kb) / args.Hkv;
   const int g = blockIdx.x % args.Hkv;
-  int k_row = kb * BN, nkv = args.Nkv - kb * BN, q_row = 0, nq = args.Nq, acc_row = 0;
+  int k_row = kb * BN, nkv = args.Nkv - kb * BN, q_row = 0, nq = args.Nq, acc_row = 0, part = -1;
+  int t0 = 0, t1 = 0;  // packed: the steps of this unit
   size_t lse_row = 0;
   if constexpr (VL) {
     pdl_wait();  // the pre-pass, with the plan, is in memory
@@ -195,12 +197,15 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     nq = u.nq;
     lse_row = padded_row(q_row, u.seq, BM);
     acc_row = int(padded_row(q_row, u.seq, kAccRows));
+    part = u.part;
+    t0 = u.tiles;
+    t1 = u.end;
   }
   const int diag = nkv - nq;  // the block's key j is visible to query i iff j <= i + diag
   const int n_qt = (nq + BM - 1) / BM;
   const int qt0 = first_q_tile(args.causal, nq, nkv);
   const int steps_per_head = qt0 < n_qt ? n_qt - qt0 : 0;
-  const int n_steps = steps_per_head * args.group;
+  const int n_steps = VL ? t1 - t0 : steps_per_head * args.group;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -234,8 +239,8 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
   const uint32_t tmem = *tmem_holder;
 
   auto step_coords = [&](int t, int& h, int& qt) {
-    h = g * args.group + t / steps_per_head;
-    qt = qt0 + t % steps_per_head;
+    h = g * args.group + (t0 + t) / steps_per_head;
+    qt = qt0 + (t0 + t) % steps_per_head;
   };
 
   if (warp == 0) {
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       bool ok = mbar_wait(kv_full, 0, abort_flag, T);
       int tails = 0;  // tiles given to the tail warp (phase of t_clean)
       // steps up to the next one whose query tile is cut off (each head's last; never, if it is whole)
-      int until_cut = VL && nq % BM != 0 ? steps_per_head : 0x7FFFFFFF;
+      int until_cut = VL && nq % BM != 0 ? steps_per_head - t0 % steps_per_head : 0x7FFFFFFF;
       if (VL && ok && nkv < BN) {
         mbar_arrive(t_land);
         ok = mbar_wait(t_clean, uint32_t(tails++ & 1), abort_flag, T);
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
       };
       bool ok = n_steps == 0 || nkv >= BN || clean(smem + OFF_K, 1, nkv);
       if (n_steps > 0 && nq % BM != 0)
-        for (int t = steps_per_head - 1; t < n_steps && ok; t += steps_per_head)  // every head's last tile
+        for (int t = steps_per_head - 1 - t0 % steps_per_head; t < n_steps && ok; t += steps_per_head)  // heads' last
           ok = clean(smem + OFF_Q0 + 2 * (t & 1) * TILE_BYTES, 2, nq % BM);
     }
   } else if (warp >= 4 + NSW) {
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     };
     bool ok = true;
     const int q_begin = qt0 * BM;  // the query tiles of a head are walked from here, head after head
-    int q0 = q_begin - BM;
+    int q0 = q_begin + (VL && n_steps > 0 ? t0 % steps_per_head : 0) * BM - BM;
     for (int t = 0; t < n_steps && ok; ++t) {
       q0 += BM;
       if (q0 >= nq) q0 = q_begin;
@@ -630,6 +635,18 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
           tmem_ld32(lane_addr + (which == 0 ? DK_COL : DV_COL) + (CPW * cw + cx) * 32, o);
           tmem_ld_wait();
           tmem_reg_fence32(o);
+          if (VL && part >= 0) {
+            // a part of the block's steps: fp32, summed with the others (and scaled) by a later kernel
+            if (key_ok) {
+              float4* dst = reinterpret_cast<float4*>(
+                  args.var_part_kv + (((size_t(part) * args.Hkv + g) * 2 + which) * BN + row) * D + (CPW * cw + cx) * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                     __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+            continue;
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -654,7 +671,7 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
                          : "memory");
           }
         }
-        if (VL && nkv < BN) continue;
+        if (VL && (nkv < BN || part >= 0)) continue;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(epi_full);
@@ -872,6 +889,7 @@ attn_status_t bwd_varlen_launch(const VarPlan& plan, const void* q, const void* 
   a.timeout_ns = kWaitLimitNs;
   a.var_units = plan.units;
   a.var_count = plan.count;
+  a.var_part_kv = plan.part_kv;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

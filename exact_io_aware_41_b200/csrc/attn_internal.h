@@ -22,21 +22,22 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
 // Packed sequences: one block of one sequence, as the plan lists them. Forward: a block of query rows, q_row and nq
 // from its first row on; where the plan cuts its keys into parts, one part of them, k_row and nkv from the part's
-// first key on. Backward: a block of keys, k_row and nkv from its first key on.
+// first key on. Backward: a block of keys, k_row and nkv from its first key on, with all or a part of its steps (the
+// query tiles of every head of a group, one after the other).
 struct __align__(16) VarUnit {
   int q_row;  // packed row of the first query
   int nq;     // the sequence's queries from that row on
   int k_row;  // packed row of the first key
   int nkv;    // the sequence's keys from that row on
-  int tiles;  // forward: key tiles of the part (at most)
-  int part;   // forward: slot of the part's result (-1: the block is whole)
+  int tiles;  // forward: key tiles of the part (at most). Backward: the first step
+  int part;   // slot of the part's result (-1: the block is whole)
   int seq;    // backward
-  int pad;
+  int end;    // backward: behind the last step
 };
 
-// A block of query rows whose parts are to be joined.
+// A block of query rows (forward) or keys (backward) whose parts are to be joined.
 struct __align__(16) VarJoin {
-  int q_row, rows;
+  int row, rows;
   int part, parts;  // first slot, and how many
 };
 
@@ -116,10 +117,11 @@ struct VarPlan {
                          // forward: count[1] query heads per L2 group, count[2] joins
   unsigned int* claim;   // 0 when the plan is made
   long long max_units;
-  // forward, where keys may be cut into parts (max_parts > 0)
+  // where blocks may be cut into parts (max_parts > 0)
   VarJoin* joins;        // [max_parts]
-  float* part_o;
-  float* part_lse;
+  float* part_o;         // forward: [max_parts][Hq][256][d]
+  float* part_lse;       // [max_parts][Hq][256]
+  float* part_kv;        // backward: [max_parts][Hkv][dK, dV][128][128]
   int max_parts;
 };
 // CTAs (or CTA pairs) that work on units at once, and the head groups into which the K/V of Tk rows would have to

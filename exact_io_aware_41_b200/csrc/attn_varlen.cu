@@ -38,6 +38,12 @@ struct PlanFwd {
     return VarUnit{s.q0 + blk * kFwdBlockRows, s.nq - blk * kFwdBlockRows, s.k0 + lo * kTileRows,
                    s.nkv - lo * kTileRows,     hi - lo,                    part, 0, 0};
   }
+  static __device__ __forceinline__ VarJoin join(const PlanSeq& s, int blk, int part, int n) {
+    return VarJoin{s.q0 + blk * kFwdBlockRows, min(kFwdBlockRows, s.nq - blk * kFwdBlockRows), part, n};
+  }
+  // Tiles of a part, at least: below that a part's own cost (its queries, the partial result, the join) outweighs
+  // what is gained.
+  static constexpr int kMinPart = 8;
 };
 // Backward: blocks of 128 keys, and the tiles of 128 query rows that block `blk` walks.
 struct PlanBwd {
@@ -46,14 +52,15 @@ struct PlanBwd {
   static __device__ __forceinline__ int tiles(const PlanSeq& s, int blk, int causal) {
     return max(0, longest(s) - first_q_tile(causal, s.nq, s.nkv - blk * kTileRows));
   }
-  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk, int, int, int) {
-    return VarUnit{s.q0, s.nq, s.k0 + blk * kTileRows, s.nkv - blk * kTileRows, 0, -1, seq, 0};
+  // steps [lo, hi) of the block's, as part `part` (-1: all of them)
+  static __device__ __forceinline__ VarUnit unit(const PlanSeq& s, int seq, int blk, int lo, int hi, int part) {
+    return VarUnit{s.q0, s.nq, s.k0 + blk * kTileRows, s.nkv - blk * kTileRows, lo, part, seq, hi};
   }
+  static __device__ __forceinline__ VarJoin join(const PlanSeq& s, int blk, int part, int n) {
+    return VarJoin{s.k0 + blk * kTileRows, min(kTileRows, s.nkv - blk * kTileRows), part, n};
+  }
+  static constexpr int kMinPart = 3;
 };
-
-// Tiles of a part, at least: below that a part's own cost (its queries, the partial result, the join) outweighs what
-// is gained (measured with 4, 8 and 16).
-constexpr int kMinPartTiles = 8;
 
 // First tile of the k-th of n parts of t tiles (t below 2^24, n below 256).
 __device__ __forceinline__ int cut_at(int k, int t, int n) { return int(unsigned(k) * unsigned(t) / unsigned(n)); }
@@ -61,17 +68,20 @@ __device__ __forceinline__ int cut_at(int k, int t, int n) { return int(unsigned
 // The plan, by one block of kPlanThreads threads. Returns the tiles of all blocks (to thread 0) and the most that
 // one block walks at most.
 //
-// share > 0 (forward, few blocks): a block is cut into parts of about max(kMinPartTiles, share-th of all tiles) by
-// rounding, where that gives two or more. With x = its tiles / that size such a block has at most 4 x / 3 parts and
-// x - 1/2 of them beyond the first, and the x sum to at most `share`: so at most 4 share / 3 parts are joined, and
-// at most `share` units are listed beyond one per block.
+// A block's work is its tiles times `heads` (backward: the heads of a group that it walks one after the other).
+//
+// share > 0 (few blocks): a block is cut into parts of about max(kMinPart, share-th of all the work) by rounding,
+// where that gives two or more. With x = its work / that size such a block has at most 4 x / 3 parts and x - 1/2 of
+// them beyond the first, and the x sum to at most `share`: so at most 4 share / 3 parts are joined, and at most
+// `share` units are listed beyond one per block.
 struct PlanSum {
   unsigned long long tiles;
   int longest;
 };
 template <class P>
 __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S,
-                                             int Tq, int Tk, int causal, int share, const VarPlan& plan) {
+                                             int Tq, int Tk, int causal, int heads, int share,
+                                             const VarPlan& plan) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // ---- check the offsets, and the largest number of tiles
   __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32], most;
@@ -108,7 +118,7 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   mx = __reduce_max_sync(0xffffffffu, mx);
   if (lane == 0) atomicMax(&most, mx);
   __syncthreads();
-  const int max_tiles = most;
+  const int max_tiles = most * heads;
   auto bin_of = [&](int tiles) -> int {  // 0: heaviest
     return max_tiles < kPlanBins ? max_tiles - tiles : int((long long)(max_tiles - tiles) * (kPlanBins - 1) / max_tiles);
   };
@@ -131,7 +141,7 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   };
   unsigned long long tiles = 0;
   each_block([&](int, const PlanSeq& q, int i) {
-    const int t = P::tiles(q, i, causal);
+    const int t = P::tiles(q, i, causal) * heads;
     tiles += t;
     if (share == 0) atomicAdd(&bins[bin_of(t)], 1);
   });
@@ -141,9 +151,9 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   __syncthreads();
   int part_tiles = 0x7FFFFFFF;
   if (share > 0) {
-    part_tiles = int(min(0x3FFFFFFFull, max((unsigned long long)kMinPartTiles, (sum + share - 1) / share)));
+    part_tiles = int(min(0x3FFFFFFFull, max((unsigned long long)P::kMinPart, (sum + share - 1) / share)));
     each_block([&](int, const PlanSeq& q, int i) {
-      const int t = P::tiles(q, i, causal), n = max(1, (t + part_tiles / 2) / part_tiles);
+      const int t = P::tiles(q, i, causal) * heads, n = max(1, (t + part_tiles / 2) / part_tiles);
       for (int k = 0; k < n; ++k) atomicAdd(&bins[bin_of(cut_at(k + 1, t, n) - cut_at(k, t, n))], 1);
     });
     __syncthreads();
@@ -172,14 +182,12 @@ __device__ __forceinline__ PlanSum make_plan(const int32_t* __restrict__ cu_q, c
   }
   __syncthreads();
   each_block([&](int seq, const PlanSeq& q, int i) {
-    const int t = P::tiles(q, i, causal), n = share > 0 ? max(1, (t + part_tiles / 2) / part_tiles) : 1;
+    const int t = P::tiles(q, i, causal) * heads, n = share > 0 ? max(1, (t + part_tiles / 2) / part_tiles) : 1;
     int part = -1;
     if (n > 1) {
       part = atomicAdd(&parts_given, n);
       if (part + n > plan.max_parts) return;  // (cannot be: see above)
-      const PlanSeq& s = q;
-      plan.joins[atomicAdd(&joins_given, 1)] =
-          VarJoin{s.q0 + i * kFwdBlockRows, min(kFwdBlockRows, s.nq - i * kFwdBlockRows), part, n};
+      plan.joins[atomicAdd(&joins_given, 1)] = P::join(q, i, part, n);
     }
     for (int k = 0; k < n; ++k) {
       const int lo = cut_at(k, t, n), hi = cut_at(k + 1, t, n);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     varlen_plan_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, int S, int Tq, int Tk,
                        int causal, int Hq, int Hkv, int groups, int ctas, int share, VarPlan plan) {
   pdl_launch();
-  const PlanSum sum = make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, share, plan);
+  const PlanSum sum = make_plan<PlanFwd>(cu_q, cu_k, S, Tq, Tk, causal, 1, share, plan);
   // `groups` groups of heads, one after the other, would keep each group's K/V in L2; but every group ends with its
   // own longest blocks still running, so no more of them than leave each CTA half as much again as the longest
   // block in every group. Measured: sixteen causal sequences of 4096 with 16 heads 1000 us in 6 groups, 1140 us in
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
     }
     const float inv = z != 0.f ? 1.f / z : 0.f;
-    __nv_bfloat16* dst = o + (size_t(j.q_row + r) * Hq + h) * D + lane * EPL;
+    __nv_bfloat16* dst = o + (size_t(j.row + r) * Hq + h) * D + lane * EPL;
     if constexpr (EPL == 1) {
       dst[0] = __float2bfloat16_rn(acc[0] * inv);
     } else {
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       for (int e = 0; e < EPL; e += 2)
         *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
     }
-    if (lane == 0) lse[size_t(h) * Tq + j.q_row + r] = z != 0.f ? mx + logf(z) : -INFINITY;
+    if (lane == 0) lse[size_t(h) * Tq + j.row + r] = z != 0.f ? mx + logf(z) : -INFINITY;
   }
 }
 
@@ -298,7 +306,7 @@ VarPlan plan_at(void* workspace, long long max_units) {
 // parts cost up to 39 MB of workspace and a kernel to join them, which many blocks, or short ones, do not pay back.
 int fwd_share(int S, int Tq, int Tk, int Hq, int d) {
   const int ctas = fwd_varlen_ctas(d);
-  if (Tk < 2 * kMinPartTiles * kTileRows || fwd_max_blocks(S, Tq) * Hq > 4ll * ctas) return 0;
+  if (Tk < 2 * PlanFwd::kMinPart * kTileRows || fwd_max_blocks(S, Tq) * Hq > 2ll * ctas) return 0;
   return ctas / Hq;
 }
 
@@ -354,11 +362,11 @@ struct BwdSpace {
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                           const float* __restrict__ lse, const int32_t* __restrict__ cu_q,
-                          const int32_t* __restrict__ cu_k, int S, int Tq, int Tk, int Hq, int causal, VarPlan plan,
-                          BwdSpace w) {
+                          const int32_t* __restrict__ cu_k, int S, int Tq, int Tk, int Hq, int Hkv, int causal, int share,
+                          VarPlan plan, BwdSpace w) {
   pdl_launch();
   if (blockIdx.x == 0) {
-    make_plan<PlanBwd>(cu_q, cu_k, S, Tq, Tk, causal, 0, plan);
+    make_plan<PlanBwd>(cu_q, cu_k, S, Tq, Tk, causal, Hq / Hkv, share, plan);
     return;
   }
   const int lane = threadIdx.x & 31, seg = lane & 15;
@@ -404,36 +412,61 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// dQ = scale * accumulator, bf16, for the rows that a sequence owns: a warp per packed row, all heads.
+// dQ = scale * accumulator, bf16, for the rows that a sequence owns (a warp per packed row, all heads); and dK, dV of
+// the key blocks whose steps were cut into parts: the parts summed in order, a warp per row.
 constexpr int kPostThreads = 256;
 __global__ void __launch_bounds__(kPostThreads)
-    varlen_bwd_post_kernel(const int* count, const float* acc, const int32_t* row_of, __nv_bfloat16* __restrict__ dq,
-                           int Tq, int Hq, float scale) {
+    varlen_bwd_post_kernel(VarPlan plan, BwdSpace w, __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
+                           __nv_bfloat16* __restrict__ dv, int Tq, int Hq, int Hkv, float scale) {
   pdl_wait();
-  if (*count < 0) return;
+  if (*plan.count < 0) return;
   const int per_row = Hq * (bwd::D / 4), lane = threadIdx.x & 31;
-  const int n_warps = int(gridDim.x) * (kPostThreads / 32);
-  for (long long t = blockIdx.x * (kPostThreads / 32) + (threadIdx.x >> 5); t < Tq; t += n_warps) {
-    const int r = row_of[t];
+  const int n_warps = int(gridDim.x) * (kPostThreads / 32), first = blockIdx.x * (kPostThreads / 32) + (threadIdx.x >> 5);
+  auto bf16x4 = [](const float4& v, float f) {
+    return make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+  };
+  for (long long t = first; t < Tq; t += n_warps) {
+    const int r = w.row_of[t];
     if (r < 0) continue;
-    const float4* src = reinterpret_cast<const float4*>(acc) + size_t(r) * per_row;
+    const float4* src = reinterpret_cast<const float4*>(w.acc) + size_t(r) * per_row;
     uint2* dst = reinterpret_cast<uint2*>(dq) + size_t(t) * per_row;
 #pragma unroll 4
-    for (int e = lane; e < per_row; e += 32) {
-      const float4 v = src[e];
-      dst[e] = make_uint2(pack_bf16x2(v.x * scale, v.y * scale), pack_bf16x2(v.z * scale, v.w * scale));
+    for (int e = lane; e < per_row; e += 32) dst[e] = bf16x4(src[e], scale);
+  }
+  const long long rows = (long long)plan.count[2] * Hkv * 2 * kTileRows;
+  for (long long i = first; i < rows; i += n_warps) {
+    const int r = int(i % kTileRows), which = int(i / kTileRows % 2), g = int(i / kTileRows / 2 % Hkv);
+    const VarJoin j = plan.joins[i / kTileRows / 2 / Hkv];
+    if (r >= j.rows) continue;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < j.parts; ++s) {
+      const float4 v = reinterpret_cast<const float4*>(
+          plan.part_kv + (((size_t(j.part + s) * Hkv + g) * 2 + which) * kTileRows + r) * bwd::D)[lane];
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
     }
+    reinterpret_cast<uint2*>((which ? dv : dk) + (size_t(j.row + r) * Hkv + g) * bwd::D)[lane] =
+        bf16x4(sum, which ? 1.f : scale);
   }
 }
 
+// Backward: shares of the steps for key blocks to be cut, as fwd_share (a part costs 128 KB of workspace per kv head
+// and its own set-up, about as long as a step).
+int bwd_share(int S, int Tq, int Tk, int Hq, int Hkv) {
+  const int ctas = fwd_varlen_ctas(bwd::D);
+  if (bwd_max_blocks(S, Tk) * Hkv > 2ll * ctas || ((long long)Tq / kTileRows + 1) * (Hq / Hkv) >= (1 << 24)) return 0;
+  return ctas / Hkv;
+}
+
 // The backward workspace: its size (workspace null), or where its parts are.
-size_t bwd_space(void* workspace, int S, int Tq, int Tk, int Hq, VarPlan* plan, BwdSpace* w) {
-  const long long max_blocks = bwd_max_blocks(S, Tk);
+size_t bwd_space(void* workspace, int S, int Tq, int Tk, int Hq, int Hkv, int share, VarPlan* plan, BwdSpace* w) {
+  const long long max_blocks = bwd_max_blocks(S, Tk) + share;
+  const int max_parts = share > 0 ? 4 * share / 3 + 1 : 0;
   w->acc_rows = ((long long)Tq / kAccRows + S) * kAccRows;
   w->lse_rows = ((long long)Tq / kTileRows + S) * kTileRows;
   const size_t acc = up256(plan_bytes(max_blocks)), lse2 = acc + up256(size_t(w->acc_rows) * Hq * bwd::D * sizeof(float)),
                dd = lse2 + up256(size_t(w->lse_rows) * Hq * sizeof(float)),
-               row_of = dd + up256(size_t(w->lse_rows) * Hq * sizeof(float));
+               row_of = dd + up256(size_t(w->lse_rows) * Hq * sizeof(float)), joins = row_of + up256(size_t(Tq) * sizeof(int32_t)),
+               part_kv = joins + up256(max_parts * sizeof(VarJoin));
   if (workspace != nullptr) {
     char* b = static_cast<char*>(workspace);
     *plan = plan_at(workspace, max_blocks);
@@ -441,8 +474,11 @@ size_t bwd_space(void* workspace, int S, int Tq, int Tk, int Hq, VarPlan* plan, 
     w->lse2 = reinterpret_cast<float*>(b + lse2);
     w->dd = reinterpret_cast<float*>(b + dd);
     w->row_of = reinterpret_cast<int32_t*>(b + row_of);
+    plan->joins = reinterpret_cast<VarJoin*>(b + joins);
+    plan->part_kv = reinterpret_cast<float*>(b + part_kv);
+    plan->max_parts = max_parts;
   }
-  return row_of + up256(size_t(Tq) * sizeof(int32_t));
+  return part_kv + size_t(max_parts) * Hkv * 2 * kTileRows * bwd::D * sizeof(float);
 }
 
 // Rows `stride` elements apart that hold heads * d dense elements: 16-byte aligned rows, and byte offsets
@@ -513,11 +549,11 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const
   }
 }
 
-size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d) {
-  if (S < 1 || Tq < 1 || Tk < 1 || Hq < 1 || d < 1 || S > kVarMaxSeqs) return 0;
+size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int Hkv, int d) {
+  if (S < 1 || Tq < 1 || Tk < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || S > kVarMaxSeqs) return 0;
   VarPlan plan;
   BwdSpace w;
-  return bwd_space(nullptr, S, Tq, Tk, Hq, &plan, &w);
+  return bwd_space(nullptr, S, Tq, Tk, Hq, Hkv, bwd_share(S, Tq, Tk, Hq, Hkv), &plan, &w);
 }
 
 attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -531,11 +567,12 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
   if (st != ATTN_OK) return st;
   if (d != 128) return ATTN_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      workspace_bytes < attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d))
+      workspace_bytes < attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, Hkv, d))
     return ATTN_ERR_WORKSPACE;
   VarPlan plan;
   BwdSpace w;
-  bwd_space(workspace, S, Tq, Tk, Hq, &plan, &w);
+  const int share = bwd_share(S, Tq, Tk, Hq, Hkv);
+  bwd_space(workspace, S, Tq, Tk, Hq, Hkv, share, &plan, &w);
   // tile coordinates, and the grid, are 32-bit
   if (plan.max_units * Hkv > 0x7FFFFFFFll || w.acc_rows > 0x7FFFFFFFll || w.lse_rows > 0x7FFFFFFFll)
     return ATTN_ERR_UNSUPPORTED;
@@ -546,12 +583,14 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
   const unsigned rows_grid = unsigned(want < 2ll * sms ? want : 2ll * sms);
   varlen_bwd_pre_kernel<<<1 + rows_grid, kPlanThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, cu_q, cu_k, S, Tq, Tk, Hq,
-      causal, plan, w);
+      Hkv, causal, share, plan, w);
   if (cudaPeekAtLastError() != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
   st = bwd_varlen_launch(plan, q, k, v, dout, dk, dv, w.acc, w.acc_rows, w.lse2, w.dd, w.lse_rows, Tq, Tk, Hq, Hkv,
                          q_stride, k_stride, v_stride, scale, causal, stream);
   if (st != ATTN_OK) return st;
-  const long long post = ((long long)Tq + kPostThreads / 32 - 1) / (kPostThreads / 32);
+  // a warp per row; with parts to join, every SM
+  long long post = ((long long)Tq + kPostThreads / 32 - 1) / (kPostThreads / 32);
+  if (share > 0 && post < 4ll * sms) post = 4ll * sms;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -561,9 +600,9 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
   lc.stream = stream;
   lc.attrs = at;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, varlen_bwd_post_kernel, static_cast<const int*>(plan.count),
-                         static_cast<const float*>(w.acc), static_cast<const int32_t*>(w.row_of),
-                         static_cast<__nv_bfloat16*>(dq), Tq, Hq, scale) != cudaSuccess)
+  if (cudaLaunchKernelEx(&lc, varlen_bwd_post_kernel, plan, w, static_cast<__nv_bfloat16*>(dq),
+                         static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), Tq, Hq, Hkv,
+                         scale) != cudaSuccess)
     return cudaGetLastError(), ATTN_ERR_CUDA;
   return ATTN_OK;
 }

@@ -238,11 +238,11 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const
  *   lse [Hq, Tq] fp32 (from attn_fwd_varlen), all read only
  *   dq [Tq, Hq, d], dk, dv [Tk, Hkv, d] bf16, dense, written: every row that a sequence owns (0 where
  *        nothing depends on it); the other rows are left as they were
- *   workspace   at least attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d) bytes, 256-byte aligned, no
+ *   workspace   at least attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, Hkv, d) bytes, 256-byte aligned, no
  *        initialisation needed
  *   d = 128 (ATTN_ERR_UNSUPPORTED otherwise); everything else as attn_fwd_varlen.
  */
-size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d);
+size_t attn_bwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int Hkv, int d);
 attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
                               const void* dout, const int32_t* cu_q, const int32_t* cu_k, void* dq, void* dk, void* dv,
                               int S, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride, long long k_stride,

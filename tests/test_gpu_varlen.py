@@ -146,6 +146,9 @@ BACKWARD = [
     ([300, 5, 129], [100, 260, 0], 2, 1),
     ([0, 64, 200, 3], [77, 640, 201, 129], 4, 1),
     ([384, 300], [10, 300], 2, 1),
+    ([1500], [1400], 8, 1),                     # few key blocks with many steps: each cut into parts
+    ([2500, 3], [130, 40], 2, 2),
+    ([40] * 300, [40] * 300, 2, 2),             # many blocks, none of them cut
 ]
 
 
@@ -293,7 +296,7 @@ def test_graph_replays_with_new_offsets(lib):
     q, k, v, do = (torch.empty((T, h, d), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv, Hq))
     cu = offsets([200, 200, 200])
     ws = torch.empty(lib.attn_fwd_varlen_workspace_bytes(3, T, T, Hq, d), dtype=torch.uint8, device="cuda")
-    ws_b = torch.empty(lib.attn_bwd_varlen_workspace_bytes(3, T, T, Hq, d), dtype=torch.uint8, device="cuda")
+    ws_b = torch.empty(lib.attn_bwd_varlen_workspace_bytes(3, T, T, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
     o, lse = torch.empty_like(q), torch.empty((Hq, T), device="cuda")
     g = [torch.empty_like(t) for t in (q, k, v)]
 

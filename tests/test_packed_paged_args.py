@@ -57,7 +57,7 @@ def test_packed_backward_refusals(c):
     for bad in (dict(S=0), dict(Tq=0), dict(Tk=0), dict(Hq=5), dict(scale=-1.0), dict(causal=-1), dict(qs=500)):
         assert call(**bad) == pkg.ATTN_ERR_INVALID_ARG, bad
     assert call(d=64, qs=256, ks=128, vs=128) == pkg.ATTN_ERR_UNSUPPORTED
-    need = lib.attn_bwd_varlen_workspace_bytes(2, 16, 16, 4, 128)
+    need = lib.attn_bwd_varlen_workspace_bytes(2, 16, 16, 4, 2, 128)
     for bad in (dict(ws=0), dict(ws=P + 128), dict(n=need - 1)):
         assert call(**bad) == pkg.ATTN_ERR_WORKSPACE, bad
 
@@ -108,7 +108,8 @@ def test_workspace_sizes(c):
     pkg, _ = c
     assert pkg.attn_fwd_varlen_workspace_bytes(0, 16, 16, 4, 64) == 0
     assert pkg.attn_fwd_varlen_workspace_bytes(3, 0, 16, 4, 64) == 0
-    assert pkg.attn_bwd_varlen_workspace_bytes(1, 0, 1, 1, 128) == 0
+    assert pkg.attn_bwd_varlen_workspace_bytes(1, 0, 1, 1, 1, 128) == 0
+    assert pkg.attn_bwd_varlen_workspace_bytes(1, 1, 1, 3, 2, 128) == 0
     assert pkg.attn_decode_paged_workspace_bytes(2, 3, 2, 64) == 0
     # a list of 3 + 300 blocks of 32 bytes (and the counters); room for parts only with few blocks and many keys
     assert pkg.attn_fwd_varlen_workspace_bytes(300, 1000, 1000, 8, 64) == 256 + 256 * math.ceil(303 * 32 / 256)
