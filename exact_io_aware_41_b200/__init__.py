@@ -9,6 +9,7 @@ how to build it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -342,60 +343,69 @@ def attn_bwd(q, k, v, o, lse, dout, scale: float | None = None, causal: bool = F
 # checks below look at each tensor once and build no strings or contexts on the way of a call that is right.
 
 def _elsewhere(device, stream):
-    """None if the call runs on the current device and stream, else the context it runs in."""
+    """The context of a call that does not run on the current device and stream."""
     import torch
 
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
+    if stream is None:
         return torch.cuda.device(device)
-    return None
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _current_stream(device) -> int:
-    import torch
+def _cuda_index(name, t):
+    """The device of a call's first tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
 
-    return torch._C._cuda_getCurrentRawStream(device.index)
 
-
-def _token_rows(name, t, bf16, device):
+def _token_rows(name, t, bf16, index):
     """Checks a bf16 [tokens, heads, d] operand whose tokens may be a stride apart; returns that stride."""
-    if t.dtype is not bf16 or t.dim() != 3 or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a 3-d bf16 CUDA tensor on {device}")
-    n, h, d = t.shape
+    if t.dtype is not bf16 or t.dim() != 3 or t.get_device() != index:
+        raise ValueError(f"{name} must be a 3-d bf16 CUDA tensor on device {index}")
     if t.is_contiguous():
-        return h * d
+        return t.size(1) * t.size(2)
+    n, h, d = t.shape
     sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
     return sn if n > 1 else h * d
 
 
-def _dense(name, t, dtype, shape, device):
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _dense(name, t, dtype, shape, index):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {index}")
 
 
-def _indices(name, t, int32, ndim, device):
-    if t.dtype is not int32 or t.device != device or t.dim() != ndim or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {ndim}-d int32 tensor on {device}")
+def _indices(name, t, int32, ndim, index):
+    if t.dtype is not int32 or t.get_device() != index or t.dim() != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ndim}-d int32 tensor on device {index}")
 
 
-def _space(workspace, device):
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+def _space(workspace, index):
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {index}")
 
 
-def _offsets_of(cu_q, cu_k, int32, device):
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(entry, index, *sizes):
+    """What the library says for these sizes on the current device, `index` (the sizes depend on its SM count)."""
+    n = int(getattr(lib_handle(), entry)(*sizes))
+    return max(n, 16)
+
+
+def _offsets_of(cu_q, cu_k, int32, index):
     """Number of sequences, after a look at both offset arrays."""
-    _indices("cu_seqlens_q", cu_q, int32, 1, device)
+    _indices("cu_seqlens_q", cu_q, int32, 1, index)
+    S = cu_q.size(0) - 1
     if cu_k is not cu_q:
-        _indices("cu_seqlens_k", cu_k, int32, 1, device)
-    S = cu_q.shape[0] - 1
-    if S < 1 or cu_k.shape[0] != S + 1:
-        raise ValueError("cu_seqlens_q and cu_seqlens_k must have one entry more than there are sequences")
+        _indices("cu_seqlens_k", cu_k, int32, 1, index)
+        if cu_k.size(0) != S + 1:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
+    if S < 1:
+        raise ValueError("cu_seqlens must have one entry more than there are sequences")
     return S
 
 
@@ -414,40 +424,42 @@ def attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale: float | Non
     """
     import torch
 
-    dev = q.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    index = _cuda_index("q", q)
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _elsewhere(q.device, stream):
             return attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, workspace, out, lse)
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     bf16 = torch.bfloat16
-    qs = _token_rows("q", q, bf16, dev)
-    ks = _token_rows("k", k, bf16, dev)
-    vs = _token_rows("v", v, bf16, dev)
+    qs = _token_rows("q", q, bf16, index)
+    ks = _token_rows("k", k, bf16, index)
+    vs = _token_rows("v", v, bf16, index)
     Tq, Hq, d = q.shape
     Tk, Hkv, dk = k.shape
     if k.shape != v.shape or dk != d:
         raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
-    S = _offsets_of(cu_seqlens_q, cu_seqlens_k, torch.int32, dev)
-    lib = lib_handle()
+    S = _offsets_of(cu_seqlens_q, cu_seqlens_k, torch.int32, index)
+    dev = q.device
     if out is None:
-        out = torch.empty((Tq, Hq, d), dtype=bf16, device=dev)
+        out = torch.empty(Tq, Hq, d, dtype=bf16, device=dev)
     else:
-        _dense("out", out, bf16, q.shape, dev)
+        _dense("out", out, bf16, q.shape, index)
     if lse is None:
-        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
+        lse = torch.empty(Hq, Tq, dtype=torch.float32, device=dev)
     else:
-        _dense("lse", lse, torch.float32, (Hq, Tq), dev)
+        _dense("lse", lse, torch.float32, (Hq, Tq), index)
     if workspace is None:
-        workspace = torch.empty(lib.attn_fwd_varlen_workspace_bytes(S, Tq, Tk, Hq, d), dtype=torch.uint8, device=dev)
+        n = _workspace_bytes("attn_fwd_varlen_workspace_bytes", index, S, Tq, Tk, Hq, d)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
-        _space(workspace, dev)
-    code = lib.attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
-                               cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks,
-                               vs, d ** -0.5 if scale is None else scale, 1 if causal else 0, workspace.data_ptr(),
-                               workspace.nbytes, _current_stream(dev))
-    _check("attn_fwd_varlen", code)
+        _space(workspace, index)
+    code = lib_handle().attn_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
+                                        cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Tq, Tk, Hq, Hkv, d,
+                                        qs, ks, vs, d ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                        workspace.data_ptr(), workspace.nbytes,
+                                        torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _check("attn_fwd_varlen", code)
     return out, lse
 
 
@@ -461,61 +473,63 @@ def attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k=None, scal
     returned them, dout [Tq, Hq, d] like o. Returns (dQ, dK, dV), dense, in the shapes of q, k, v."""
     import torch
 
-    dev = q.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    index = _cuda_index("q", q)
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _elsewhere(q.device, stream):
             return attn_bwd_varlen(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale, causal, workspace, dq, dk,
                                    dv)
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     bf16 = torch.bfloat16
-    qs = _token_rows("q", q, bf16, dev)
-    ks = _token_rows("k", k, bf16, dev)
-    vs = _token_rows("v", v, bf16, dev)
+    qs = _token_rows("q", q, bf16, index)
+    ks = _token_rows("k", k, bf16, index)
+    vs = _token_rows("v", v, bf16, index)
     Tq, Hq, d = q.shape
     Tk, Hkv, d_k = k.shape
     if k.shape != v.shape or d_k != d:
         raise ValueError("k and v must be [Tk, Hkv, d] with q's d")
-    S = _offsets_of(cu_seqlens_q, cu_seqlens_k, torch.int32, dev)
-    _dense("o", o, bf16, q.shape, dev)
-    _dense("dout", dout, bf16, q.shape, dev)
-    _dense("lse", lse, torch.float32, (Hq, Tq), dev)
-    lib = lib_handle()
+    S = _offsets_of(cu_seqlens_q, cu_seqlens_k, torch.int32, index)
+    _dense("o", o, bf16, q.shape, index)
+    _dense("dout", dout, bf16, q.shape, index)
+    _dense("lse", lse, torch.float32, (Hq, Tq), index)
+    dev = q.device
     if dq is None:
-        dq = torch.empty_like(o)
+        dq = torch.empty(Tq, Hq, d, dtype=bf16, device=dev)
     else:
-        _dense("dq", dq, bf16, q.shape, dev)
+        _dense("dq", dq, bf16, q.shape, index)
     if dk is None:
-        dk = torch.empty((Tk, Hkv, d), dtype=bf16, device=dev)
+        dk = torch.empty(Tk, Hkv, d, dtype=bf16, device=dev)
     else:
-        _dense("dk", dk, bf16, k.shape, dev)
+        _dense("dk", dk, bf16, k.shape, index)
     if dv is None:
-        dv = torch.empty_like(dk)
+        dv = torch.empty(Tk, Hkv, d, dtype=bf16, device=dev)
     else:
-        _dense("dv", dv, bf16, k.shape, dev)
+        _dense("dv", dv, bf16, k.shape, index)
     if workspace is None:
-        workspace = torch.empty(lib.attn_bwd_varlen_workspace_bytes(S, Tq, Tk, Hq, Hkv, d), dtype=torch.uint8,
-                                device=dev)
+        n = _workspace_bytes("attn_bwd_varlen_workspace_bytes", index, S, Tq, Tk, Hq, Hkv, d)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
-        _space(workspace, dev)
-    code = lib.attn_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-                               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                               dv.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
-                               1 if causal else 0, workspace.data_ptr(), workspace.nbytes, _current_stream(dev))
-    _check("attn_bwd_varlen", code)
+        _space(workspace, index)
+    code = lib_handle().attn_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                        dout.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+                                        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), S, Tq, Tk, Hq, Hkv, d, qs, ks, vs,
+                                        d ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                        workspace.data_ptr(), workspace.nbytes,
+                                        torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _check("attn_bwd_varlen", code)
     return dq, dk, dv
 
 
-def _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, int32, dev):
-    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype is not bf16 or t.device != dev or t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous [n_pages, page_size, Hkv, d] bf16 CUDA tensor on {dev}")
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must have the same shape")
-    _indices("page_table", page_table, int32, 2, dev)
-    _indices("kv_lens", kv_lens, int32, 1, dev)
-    if page_table.shape[0] != kv_lens.shape[0]:
+def _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, int32, index):
+    if (k_pages.dtype is not bf16 or v_pages.dtype is not bf16 or k_pages.dim() != 4 or k_pages.shape != v_pages.shape
+            or k_pages.get_device() != index or v_pages.get_device() != index or not k_pages.is_contiguous()
+            or not v_pages.is_contiguous()):
+        raise ValueError("k_pages and v_pages must be contiguous [n_pages, page_size, Hkv, d] bf16 tensors of the same "
+                         f"shape on device {index}")
+    _indices("page_table", page_table, int32, 2, index)
+    _indices("kv_lens", kv_lens, int32, 1, index)
+    if page_table.size(0) != kv_lens.size(0):
         raise ValueError("page_table must be [B, max_pages] and kv_lens [B]")
     return k_pages.shape
 
@@ -534,35 +548,38 @@ def attn_decode_paged(q, k_pages, v_pages, page_table, kv_lens, scale: float | N
     """
     import torch
 
-    dev = q.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    index = _cuda_index("q", q)
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _elsewhere(q.device, stream):
             return attn_decode_paged(q, k_pages, v_pages, page_table, kv_lens, scale, workspace, out, lse)
     bf16 = torch.bfloat16
-    qs = _token_rows("q", q, bf16, dev)
-    n_pages, page_size, Hkv, d_k = _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, torch.int32, dev)
+    qs = _token_rows("q", q, bf16, index)
+    n_pages, page_size, Hkv, d_k = _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, torch.int32, index)
     B, Hq, d = q.shape
-    if d_k != d or kv_lens.shape[0] != B:
+    B_t, max_pages = page_table.shape
+    if d_k != d or B_t != B:
         raise ValueError("k_pages must have q's d, kv_lens and page_table q's B")
-    lib = lib_handle()
+    dev = q.device
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=bf16, device=dev)
+        out = torch.empty(B, Hq, d, dtype=bf16, device=dev)
     else:
-        _dense("out", out, bf16, q.shape, dev)
+        _dense("out", out, bf16, q.shape, index)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
     else:
-        _dense("lse", lse, torch.float32, (B, Hq), dev)
+        _dense("lse", lse, torch.float32, (B, Hq), index)
     if workspace is None:
-        workspace = torch.empty(lib.attn_decode_paged_workspace_bytes(B, Hq, Hkv, d), dtype=torch.uint8, device=dev)
+        n = _workspace_bytes("attn_decode_paged_workspace_bytes", index, B, Hq, Hkv, d)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
-        _space(workspace, dev)
-    code = lib.attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                                 kv_lens.data_ptr(), n_pages, page_size, page_table.shape[1], out.data_ptr(),
-                                 lse.data_ptr(), B, Hq, Hkv, d, qs, d ** -0.5 if scale is None else scale,
-                                 workspace.data_ptr(), workspace.nbytes, _current_stream(dev))
-    _check("attn_decode_paged", code)
+        _space(workspace, index)
+    code = lib_handle().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                          kv_lens.data_ptr(), n_pages, page_size, max_pages, out.data_ptr(),
+                                          lse.data_ptr(), B, Hq, Hkv, d, qs, d ** -0.5 if scale is None else scale,
+                                          workspace.data_ptr(), workspace.nbytes,
+                                          torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _check("attn_decode_paged", code)
     return out, lse
 
 
@@ -572,26 +589,27 @@ def attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_se
     are the lengths with the new rows, so the last of them becomes token kv_lens[b] - 1."""
     import torch
 
-    dev = k_pages.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    index = _cuda_index("k_pages", k_pages)
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _elsewhere(k_pages.device, stream):
             return attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, kv_lens, cu_seqlens)
     bf16 = torch.bfloat16
-    n_pages, page_size, Hkv, d = _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, torch.int32, dev)
-    ks = _token_rows("k_new", k_new, bf16, dev)
-    vs = _token_rows("v_new", v_new, bf16, dev)
+    n_pages, page_size, Hkv, d = _pool_shape(k_pages, v_pages, page_table, kv_lens, bf16, torch.int32, index)
+    ks = _token_rows("k_new", k_new, bf16, index)
+    vs = _token_rows("v_new", v_new, bf16, index)
     T, H, dn = k_new.shape
-    B = kv_lens.shape[0]
+    B, max_pages = page_table.shape
     if k_new.shape != v_new.shape or H != Hkv or dn != d:
         raise ValueError("k_new and v_new must be [T, Hkv, d] with the pool's Hkv and d")
     cu = None
     if cu_seqlens is not None:
-        _indices("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
-        if cu_seqlens.shape[0] != B + 1:
+        _indices("cu_seqlens", cu_seqlens, torch.int32, 1, index)
+        if cu_seqlens.size(0) != B + 1:
             raise ValueError("cu_seqlens must be [B + 1]")
         cu = cu_seqlens.data_ptr()
     code = lib_handle().attn_cache_append(k_new.data_ptr(), v_new.data_ptr(), cu, page_table.data_ptr(),
                                           kv_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, T, n_pages,
-                                          page_size, page_table.shape[1], Hkv, d, ks, vs, _current_stream(dev))
-    _check("attn_cache_append", code)
+                                          page_size, max_pages, Hkv, d, ks, vs,
+                                          torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        _check("attn_cache_append", code)

@@ -616,12 +616,48 @@ attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStre
   return ATTN_OK;
 }
 
-// New rows into the pages of their sequences: pure copies. A block takes `rows` consecutive packed rows:
-// its first threads look up where each of them goes (the sequence by bisection of the offsets, the page
-// from the table; -1 for a row that is not written), then all threads copy 16-byte units of K and V.
+// New rows into the pages of their sequences: pure copies. A block takes `rows` consecutive packed rows: every
+// thread first loads its 16-byte units of K and V, whose place in the source is known, while the block's first
+// threads look up where each row goes (the sequence by bisection of the offsets, its length, the page from the
+// table: three dependent reads; -1 for a row that is not written), and then stores them.
 // Bound by memory: every row is read and written once (2 * 2 * Hkv * d bytes per token).
-constexpr int kAppendRows = 8;   // most rows of one block
+constexpr int kAppendRows = 8;    // most rows of one block
 constexpr int kAppendThreads = 256;
+constexpr int kAppendUnits = 4;   // units of K, and of V, that a thread holds
+
+// Place (in 16-byte units of the pools) of packed row t, or -1.
+__device__ __forceinline__ long long append_place(int t, const int32_t* __restrict__ cu,
+                                                  const int32_t* __restrict__ table,
+                                                  const int32_t* __restrict__ kv_lens, int B, int T, int n_pages,
+                                                  int page_size, int max_pages, int units) {
+  if (t >= T) return -1;
+  int b = t, i = 0, n = 1;
+  if (cu != nullptr) {
+    if (t < cu[0] || t >= cu[B]) return -1;
+    int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+    i = t - cu[b];
+    n = cu[b + 1] - cu[b];
+  }
+  const long long pos = (long long)kv_lens[b] - n + i;
+  if (pos < 0 || pos >= (long long)max_pages * page_size) {
+    atomicOr(&g_error_word, kErrBadLengthBit);
+    return -1;
+  }
+  const int p = table[size_t(b) * max_pages + int(pos / page_size)];
+  if (unsigned(p) >= unsigned(n_pages)) {
+    atomicOr(&g_error_word, kErrBadPageBit);
+    return -1;
+  }
+  return ((long long)p * page_size + pos % page_size) * units;
+}
 
 __global__ void __launch_bounds__(kAppendThreads)
     cache_append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
@@ -629,53 +665,39 @@ __global__ void __launch_bounds__(kAppendThreads)
                         const int32_t* __restrict__ kv_lens, uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
                         int B, int T, int n_pages, int page_size, int max_pages, int units, long long ks_units,
                         long long vs_units, int rows) {
-  __shared__ long long dst[kAppendRows];  // 16-byte unit of the row's place in the pools, or -1
-  const int t0 = blockIdx.x * rows;
-  if (threadIdx.x < rows) {
-    const int t = t0 + threadIdx.x;
-    long long at = -1;
-    if (t < T) {
-      int b = t, i = 0, n = 1;
-      bool owned = true;
-      if (cu != nullptr) {
-        owned = t >= cu[0] && t < cu[B];
-        if (owned) {
-          int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t)
-              lo = mid;
-            else
-              hi = mid;
-          }
-          b = lo;
-          i = t - cu[b];
-          n = cu[b + 1] - cu[b];
-        }
+  __shared__ long long dst[kAppendRows];  // place of each row in the pools
+  const int t0 = blockIdx.x * rows, total = min(rows, T - t0) * units;
+  uint4 k[kAppendUnits], v[kAppendUnits];
+  bool placed = false;
+  for (int base = threadIdx.x; base < total || !placed; base += kAppendUnits * kAppendThreads) {
+#pragma unroll
+    for (int i = 0; i < kAppendUnits; ++i) {
+      const int u = base + i * kAppendThreads;
+      if (u < total) {
+        const int r = u / units, c = u - r * units;
+        k[i] = k_new[(t0 + r) * ks_units + c];
+        v[i] = v_new[(t0 + r) * vs_units + c];
       }
-      if (owned) {
-        const long long pos = (long long)kv_lens[b] - n + i;
-        if (pos < 0 || pos >= (long long)max_pages * page_size) {
-          atomicOr(&g_error_word, kErrBadLengthBit);
-        } else {
-          const int p = table[size_t(b) * max_pages + int(pos / page_size)];
-          if (unsigned(p) >= unsigned(n_pages))
-            atomicOr(&g_error_word, kErrBadPageBit);
-          else
-            at = ((long long)p * page_size + pos % page_size) * units;
+    }
+    if (!placed) {  // the first time, by every thread
+      if (threadIdx.x < rows)
+        dst[threadIdx.x] =
+            append_place(t0 + threadIdx.x, cu, table, kv_lens, B, T, n_pages, page_size, max_pages, units);
+      __syncthreads();
+      placed = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kAppendUnits; ++i) {
+      const int u = base + i * kAppendThreads;
+      if (u < total) {
+        const int r = u / units, c = u - r * units;
+        const long long at = dst[r];
+        if (at >= 0) {
+          k_pages[at + c] = k[i];
+          v_pages[at + c] = v[i];
         }
       }
     }
-    dst[threadIdx.x] = at;
-  }
-  __syncthreads();
-  for (int u = threadIdx.x; u < rows * units; u += kAppendThreads) {
-    const int r = u / units, c = u - r * units;
-    const long long at = dst[r];
-    if (at < 0) continue;
-    const uint4 a = k_new[(t0 + r) * ks_units + c], b = v_new[(t0 + r) * vs_units + c];
-    k_pages[at + c] = a;
-    v_pages[at + c] = b;
   }
 }
 
