@@ -98,7 +98,7 @@ struct PagedArgs {
   int B, Hq, Hkv, G;
   long long q_stride;
   float scale_log2;
-  long long* head;   // workspace: W, N, then the entries (of one kv head) before each sequence, and all [B + 1]
+  int4* cuts;        // workspace: per CTA, if its last pair goes on in the next CTAs: (b, g, parts), else parts = 0
   float* parts;      // workspace: [2 * CTA + end] slots of PART_FLOATS
   unsigned long long timeout_ns;
 };
@@ -182,19 +182,18 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
   const long long W = total * a.Hkv;
   const long long want = (W + kPagedMinShare - 1) / kPagedMinShare;
   const long long N = want < gridDim.x ? want : gridDim.x;
-  if (blockIdx.x == 0) {
-    if (threadIdx.x == 0) {
-      a.head[0] = W;
-      a.head[1] = N;
+  // sequences without tokens are in no share: O = 0 and LSE = -inf here
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (entries_of(b) == 0) {
+      const size_t row0 = size_t(b) * a.Hq;
+      for (int e = threadIdx.x; e < a.Hq * (D / 8); e += C::THREADS)
+        reinterpret_cast<uint4*>(a.o + row0 * D)[e] = make_uint4(0, 0, 0, 0);
+      for (int h = threadIdx.x; h < a.Hq; h += C::THREADS) a.lse[row0 + h] = -INFINITY;
     }
-    long long x = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      a.head[2 + b] = x;
-      x += entries_of(b);
-      if (b == a.B - 1) a.head[2 + a.B] = x;
-    }
+  if (blockIdx.x >= N) {
+    if (threadIdx.x == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
   }
-  if (blockIdx.x >= N) return;
   const long long begin = blockIdx.x * W / N, end = (blockIdx.x + 1ll) * W / N;
   if (before * a.Hkv <= begin && begin < (before + mine) * a.Hkv) {
     long long x = before;
@@ -233,6 +232,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
     int t_first = t;  // first tile of the current segment
     int i = 0;        // tiles issued
     bool ok = true;
+    int4 cut = make_int4(0, 0, 0, 0);
     while (at < end) {
       const int nt = n - C::PAIR_COST;
       PagedTile now;
@@ -242,6 +242,12 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
       now.flags = (t == t_first ? kTileFirst : 0) | (t + 1 == nt || at + 1 == end ? kTileLast : 0) |
                   (t_first == 0 ? kTileStart : 0) | (t_first == 0 && t + 1 == nt ? kTileWhole : 0);
       const int row = int((unsigned(t) * C::TT + lane * a.box) % unsigned(a.page_size)), cur = page;
+      if (at + 1 == end && t_first == 0 && t + 1 < nt) {
+        // the pair begins here and goes on: up to the CTA that holds its last entry x, the smallest i with
+        // x < floor((i + 1) W / N)
+        const long long x = at + (nt - 1 - t);
+        cut = make_int4(b, g, int(min(N - 1, ((x + 1) * N - 1) / W) - blockIdx.x) + 1, 0);
+      }
       // the next tile and its pages, while the stage becomes free
       ++at;
       if (at < end) {
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
       }
       ++i;
     }
+    if (lane == 0) a.cuts[blockIdx.x] = ok ? cut : make_int4(0, 0, 0, 0);
     const int st = i % C::STAGES;
     if (ok && lane == 0 && (ok = mbar_wait(&empty[st], uint32_t(((i / C::STAGES) & 1) ^ 1), abort_flag, T))) {
       tile_of[st].flags = kTileStop;
@@ -512,79 +519,72 @@ __global__ void __launch_bounds__(PagedCfg<D, NH>::THREADS, PagedCfg<D, NH>::CTA
   }
 }
 
-// Joins the parts of the (b, g) pairs that several CTAs shared, one block per query head row: with (m_s, l_s,
-// o_s) per part, M = max m_s, O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s, LSE = ln 2 M + ln of that sum. Each
-// warp takes every NWARP-th part with a running maximum (one pass: all loads of a part are independent), then
-// the warps are merged; the order of the sums does not depend on timing. Rows of sequences without tokens get
-// 0 and -inf here.
-constexpr int kJoinThreads = 256;
-
-template <int D, int NH>
-__global__ void __launch_bounds__(kJoinThreads)
-    decode_paged_join_kernel(const long long* head, const float* parts, __nv_bfloat16* __restrict__ o,
+// Joins the parts of the (b, g) pairs that several CTAs shared: with (m_s, l_s, o_s) per part, M = max m_s,
+// O = sum 2^(m_s - M) o_s / sum 2^(m_s - M) l_s, LSE = ln 2 M + ln of that sum. Block (c, y) takes the pair that CTA c
+// cut, if any (at most one: the last of its share), and the heads y, y + gridDim.y, ... of its group: the number of
+// blocks does not depend on the batch. The warps share a head's parts, each with a running maximum (one pass: all
+// loads of a part are independent), and are merged; the order of the sums does not depend on timing. Bound by latency:
+// after the wait for the split kernel, the cut, its parts and the merge follow each other.
+template <int D, int NH, int NWARP>
+__global__ void __launch_bounds__(32 * NWARP)
+    decode_paged_join_kernel(const int4* cuts, const float* parts, __nv_bfloat16* __restrict__ o,
                              float* __restrict__ lse, int Hkv, int G) {
   using C = PagedCfg<D, NH>;
-  constexpr int NWARP = kJoinThreads / 32, EPL = D / 32;  // elements of d per lane
+  constexpr int EPL = D / 32;  // elements of d per lane
   __shared__ float sm[NWARP], sl[NWARP], acc[NWARP][D];
-  const int row = blockIdx.x, hd = row % G, g = row / G % Hkv, b = row / G / Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const long long W = head[0], N = head[1], first = head[2 + b], n = head[3 + b] - first;
-  if (n <= 0) {
-    for (int e = threadIdx.x; e < D; e += kJoinThreads) o[size_t(row) * D + e] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0) lse[row] = -INFINITY;
-    return;
-  }
-  // the CTA that holds entry x of the list: the smallest i with x < floor((i + 1) W / N)
-  const long long x0 = first * Hkv + g * n + C::PAIR_COST, x1 = first * Hkv + (g + 1) * n - 1;  // first, last tile
-  const int c0 = int(((x0 + 1) * N - 1) / W), c1 = int(min(N - 1, ((x1 + 1) * N - 1) / W));
-  if (c0 >= c1) return;
-  float m = -INFINITY, l = 0.f, v[EPL];
+  const int4 cut = cuts[blockIdx.x];  // b, g, parts
+  for (int hd = blockIdx.y; hd < G && cut.z > 0; hd += gridDim.y) {
+    const size_t row = (size_t(cut.x) * Hkv + cut.y) * G + hd;
+    float m = -INFINITY, l = 0.f, v[EPL];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) v[e] = 0.f;
+    for (int e = 0; e < EPL; ++e) v[e] = 0.f;
 #pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += NWARP) {
-    // the first CTA's tiles start the pair (its second slot), the others' continue it
-    const float* p = parts + size_t(2 * c + (c == c0 ? 1 : 0)) * C::PART_FLOATS;
-    const float pm = p[C::HEADS * D + hd], pl = p[C::HEADS * D + C::HEADS + hd];
-    float x[EPL];
+    for (int s = warp; s < cut.z; s += NWARP) {
+      // the first CTA's tiles start the pair (its second slot), the others' continue it
+      const float* p = parts + size_t(2 * (blockIdx.x + s) + (s == 0 ? 1 : 0)) * C::PART_FLOATS;
+      const float pm = p[C::HEADS * D + hd], pl = p[C::HEADS * D + C::HEADS + hd];
+      float x[EPL];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) x[e] = p[hd * D + lane + 32 * e];
-    const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
-    const float fo = ex2(m - ref), fp = ex2(pm - ref);
-    m = mn;
-    l = fmaf(fp, pl, l * fo);
+      for (int e = 0; e < EPL; ++e) x[e] = p[hd * D + lane + 32 * e];
+      const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
+      const float fo = ex2(m - ref), fp = ex2(pm - ref);
+      m = mn;
+      l = fmaf(fp, pl, l * fo);
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) v[e] = fmaf(fp, x[e], v[e] * fo);
+      for (int e = 0; e < EPL; ++e) v[e] = fmaf(fp, x[e], v[e] * fo);
+    }
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[warp][lane + 32 * e] = v[e];
+    __syncthreads();
+    float mx = -INFINITY, z = 0.f, f[NWARP];
+#pragma unroll
+    for (int w = 0; w < NWARP; ++w) mx = fmaxf(mx, sm[w]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int w = 0; w < NWARP; ++w) {
+      f[w] = ex2(sm[w] - ref);
+      z = fmaf(f[w], sl[w], z);
+    }
+    const float inv = z != 0.f ? 1.f / z : 0.f;
+    for (int e = threadIdx.x; e < D; e += 32 * NWARP) {
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < NWARP; ++w) x = fmaf(f[w], acc[w][e], x);
+      o[row * D + e] = __float2bfloat16_rn(x * inv);
+    }
+    if (threadIdx.x == 0) lse[row] = z != 0.f ? mx * 0.6931471805599453f + logf(z) : -INFINITY;
+    __syncthreads();  // the next head's parts go to the same place
   }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[warp][lane + 32 * e] = v[e];
-  __syncthreads();
-  float mx = -INFINITY, z = 0.f, f[NWARP];
-#pragma unroll
-  for (int w = 0; w < NWARP; ++w) mx = fmaxf(mx, sm[w]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-  for (int w = 0; w < NWARP; ++w) {
-    f[w] = ex2(sm[w] - ref);
-    z = fmaf(f[w], sl[w], z);
-  }
-  const float inv = z != 0.f ? 1.f / z : 0.f;
-  for (int e = threadIdx.x; e < D; e += kJoinThreads) {
-    float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < NWARP; ++w) x = fmaf(f[w], acc[w][e], x);
-    o[size_t(row) * D + e] = __float2bfloat16_rn(x * inv);
-  }
-  if (threadIdx.x == 0) lse[row] = z != 0.f ? mx * 0.6931471805599453f + logf(z) : -INFINITY;
 }
 
-// Workspace: W, N and the entry counts, then the part slots.
-size_t paged_head_bytes(int B) { return (size_t(3 + B) * sizeof(long long) + 255) / 256 * 256; }
+// Workspace: the cuts, then the part slots.
+constexpr size_t kPagedCutBytes = kPagedMaxCtas * sizeof(int4);
 
 template <int D, int NH>
 attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStream_t stream) {
@@ -605,13 +605,17 @@ attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStre
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3(unsigned(a.B) * unsigned(a.Hq));
-  lc.blockDim = dim3(kJoinThreads);
+  lc.gridDim = dim3(grid, a.G < 4 ? a.G : 4);
+  // many pairs: each is cut into few parts, and small blocks let all of them run at once (a batch of 64, 32 heads:
+  // 91 -> 87.5 us against 16 warps); few pairs: many parts each
+  const bool many = 8ll * a.B * a.Hkv >= grid;
+  lc.blockDim = dim3(many ? 128 : 512);
   lc.stream = stream;
   lc.attrs = at;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, decode_paged_join_kernel<D, NH>, static_cast<const long long*>(a.head),
-                         static_cast<const float*>(a.parts), a.o, a.lse, a.Hkv, a.G) != cudaSuccess)
+  if (cudaLaunchKernelEx(&lc, many ? decode_paged_join_kernel<D, NH, 4> : decode_paged_join_kernel<D, NH, 16>,
+                         static_cast<const int4*>(a.cuts), static_cast<const float*>(a.parts), a.o, a.lse, a.Hkv,
+                         a.G) != cudaSuccess)
     return cudaGetLastError(), ATTN_ERR_CUDA;
   return ATTN_OK;
 }
@@ -710,7 +714,7 @@ extern "C" {
 size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return 0;
   const size_t heads = Hq / Hkv <= 8 ? 8 : 16;
-  return paged_head_bytes(B) + 2 * size_t(kPagedMaxCtas) * heads * (size_t(d) + 2) * sizeof(float);
+  return kPagedCutBytes + 2 * size_t(kPagedMaxCtas) * heads * (size_t(d) + 2) * sizeof(float);
 }
 
 attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -748,8 +752,8 @@ attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* 
   a.G = Hq / Hkv;
   a.q_stride = q_stride;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.head = static_cast<long long*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + paged_head_bytes(B));
+  a.cuts = static_cast<int4*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kPagedCutBytes);
   a.timeout_ns = kWaitLimitNs;
   const bool wide = a.G > 8;
   switch (d) {
