@@ -42,8 +42,9 @@ struct PlanFwd {
     return VarJoin{s.q0 + blk * kFwdBlockRows, min(kFwdBlockRows, s.nq - blk * kFwdBlockRows), part, n};
   }
   // Tiles of a part, at least: below that a part's own cost (its queries, the partial result, the join) outweighs
-  // what is gained.
-  static constexpr int kMinPart = 8;
+  // what is gained. d = 128, with 4 / 6 / 8 / 16: 512 queries over 4096 keys, 8 heads, 33.8 / 36.6 / 38.0 / 51.2 us;
+  // 2048 causal ones 48.5 / 40.5 / 40.3 / 43.1 us.
+  static constexpr int kMinPart = 6;
 };
 // Backward: blocks of 128 keys, and the tiles of 128 query rows that block `blk` walks.
 struct PlanBwd {
@@ -59,7 +60,10 @@ struct PlanBwd {
   static __device__ __forceinline__ VarJoin join(const PlanSeq& s, int blk, int part, int n) {
     return VarJoin{s.k0 + blk * kTileRows, min(kTileRows, s.nkv - blk * kTileRows), part, n};
   }
-  static constexpr int kMinPart = 3;
+  // Steps of a part, at least. With 2 / 3 / 6 / no parts: samples of 200 + 77 + 1 + 513, 4 heads in groups of 2,
+  // 32.3 / 35.1 / 45.0 / 49.5 us; 500 + 400 + 300, a group of 8, 38.2 / 43.1 / 57.6 / 127.6 us; 2048, 16 heads in
+  // groups of 8, 85 us with any and 380 us without.
+  static constexpr int kMinPart = 2;
 };
 
 // First tile of the k-th of n parts of t tiles (t below 2^24, n below 256).
