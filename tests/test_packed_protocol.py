@@ -1,0 +1,291 @@
+"""Models of the packed kernels' tail hand-off, run under random timings on the CPU (tests/protocol_sim.py): where a
+sequence ends inside a tile, a warp of its own zeroes the tile's rows behind the end between its landing and the
+products that sum over them.
+
+Forward (csrc/attn_fwd.cu): the MMA thread sees the unit's last V tile land, announces it (v_land), goes on, and
+waits for v_clean before the tile's PV. The tail warp walks the same units through the unit ring and waits for
+v_land only in units that are cut. Backward (csrc/attn_bwd.cu): K once, then Q and dO of every head's last step
+(t_land, t_clean), in double-buffered stages that the dQ role releases."""
+import random
+
+import pytest
+
+from protocol_sim import Hazard, Sim
+
+STAGES, SCHED = 4, 4
+
+
+def forward_tail(sim, units, no_wait=False, tail_watches_the_ring=False):
+    """units: (n, cut): K/V tiles and whether the last one is cut. Planted mistakes: the PV does not wait for the
+    tail warp; the tail warp waits for the ring's own phase of the tile instead of the MMA thread's word."""
+    for name in ("q_full", "q_empty", "s_full", "p_full", "v_land", "v_clean"):
+        sim.bar(name)
+    for s in range(STAGES):
+        sim.bar(f"kv_full{s}")
+        sim.bar(f"kv_empty{s}")
+    for i in range(SCHED):
+        sim.bar(f"sched_full{i}")
+        sim.bar(f"sched_empty{i}", 3)  # MMA thread, softmax, tail warp
+
+    def take(k):
+        slot = k % SCHED
+        yield ("wait", f"sched_full{slot}", k // SCHED)
+        yield ("access", [(f"sched{slot}", f"unit {k}")], [], 0.2)
+        yield ("arrive", f"sched_empty{slot}")
+
+    def producer():
+        pos = 0
+        for k in range(len(units) + 1):
+            slot = k % SCHED
+            yield ("wait", f"sched_empty{slot}", k // SCHED - 1)
+            yield ("access", [], [(f"sched{slot}", f"unit {k}")], 0.3)
+            yield ("arrive", f"sched_full{slot}")
+            if k == len(units):
+                break
+            for j in range(units[k][0]):
+                for kv in "KV":
+                    s = pos % STAGES
+                    yield ("wait", f"kv_empty{s}", pos // STAGES - 1)
+                    yield ("async", [], [(f"KV{s}", f"{kv}{j} u{k}")], 3.0, (lambda s=s: sim.arrive(f"kv_full{s}")))
+                    pos += 1
+
+    def mma():
+        pos, tiles, cuts = 0, 0, 0
+        for k in range(len(units) + 1):
+            yield from take(k)
+            if k == len(units):
+                break
+            n, cut = units[k]
+            for j in range(n):
+                sk, sv = pos % STAGES, (pos + 1) % STAGES
+                yield ("wait", f"kv_full{sk}", pos // STAGES)
+                yield ("mma", [(f"KV{sk}", f"K{j} u{k}")], [("S", f"S {j} u{k}")])
+                yield ("commit", "s_full")
+                yield ("commit", f"kv_empty{sk}")
+                yield ("wait", f"kv_full{sv}", (pos + 1) // STAGES)
+                last_cut = cut and j == n - 1
+                if last_cut and not tail_watches_the_ring:
+                    yield ("arrive", "v_land")
+                yield ("wait", "p_full", tiles)
+                tiles += 1
+                if last_cut and not no_wait:
+                    yield ("wait", "v_clean", cuts)
+                    cuts += 1
+                v = f"V{j} u{k}" + (" clean" if last_cut else "")
+                yield ("mma", [("S", f"P {j} u{k}"), (f"KV{sv}", v)], [("O", f"O u{k}")])
+                yield ("commit", f"kv_empty{sv}")
+                pos += 2
+
+    def softmax():
+        tiles = 0
+        for k in range(len(units) + 1):
+            yield from take(k)
+            if k == len(units):
+                break
+            for j in range(units[k][0]):
+                yield ("wait", "s_full", tiles)
+                yield ("access", [], [("S", f"P {j} u{k}")], 2.0)
+                yield ("arrive", "p_full")
+                tiles += 1
+
+    def tail():
+        pos, cuts = 0, 0
+        for k in range(len(units) + 1):
+            yield from take(k)
+            if k == len(units):
+                break
+            n, cut = units[k]
+            pos += 2 * n
+            if n == 0 or not cut:
+                continue
+            s = (pos - 1) % STAGES
+            if tail_watches_the_ring:
+                yield ("wait", f"kv_full{s}", (pos - 1) // STAGES)
+            else:
+                yield ("wait", "v_land", cuts)
+            cuts += 1
+            sim.read_begin(f"KV{s}", f"V{n - 1} u{k}")
+            sim.read_end(f"KV{s}")
+            yield ("access", [], [(f"KV{s}", f"V{n - 1} u{k} clean")], 1.0)
+            yield ("arrive", "v_clean")
+
+    roles = {"producer": producer, "mma": mma, "softmax": softmax, "tail": tail}
+    for name, role in roles.items():
+        sim.run(name, role())
+    return set(roles)
+
+
+def backward_tail(sim, heads, per_head, cut_k, cut_q, first=0, last=None, no_wait=False):
+    """A key block's steps [first, last) of heads * per_head; cut_k: its K tile is cut, cut_q: every head's last query
+    tile is. Planted mistake: dV does not wait for the tail warp."""
+    last = heads * per_head if last is None else last
+    n = last - first
+    for name in ("kv_full", "t_land", "t_clean", "q_full0", "q_full1", "q_empty0", "q_empty1", "pt_full", "st_full",
+                 "dk_done0", "dk_done1", "dq_full", "dq_free"):
+        sim.bar(name)
+    is_cut = [cut_q and (first + t) % per_head == per_head - 1 for t in range(n)]
+
+    def producer():
+        yield ("async", [], [("K", "K")], 3.0, lambda: sim.arrive("kv_full"))
+        for t in range(n):
+            if t >= 2:
+                yield ("wait", f"q_empty{t & 1}", (t - 2) >> 1)
+            yield ("async", [], [(f"Q{t & 1}", f"Q {t}")], 3.0, (lambda t=t: sim.arrive(f"q_full{t & 1}")))
+
+    def mma():
+        tails = 0
+        yield ("wait", "kv_full", 0)
+        if cut_k:
+            yield ("arrive", "t_land")
+            yield ("wait", "t_clean", tails)
+            tails += 1
+        k = "K clean" if cut_k else "K"
+        for t in range(n):
+            yield ("wait", f"q_full{t & 1}", t >> 1)
+            if is_cut[t]:
+                yield ("arrive", "t_land")
+            if t > 0:
+                yield ("wait", "dq_free", t - 1)
+            yield ("mma", [("K", k)], [("S", f"S {t}")])  # reads the cut rows too, in either state: masked later
+            yield ("commit", "st_full")
+            yield ("wait", "pt_full", t)
+            if is_cut[t] and not no_wait:
+                yield ("wait", "t_clean", tails)
+                tails += 1
+            q = f"Q {t}" + (" clean" if is_cut[t] else "")
+            yield ("mma", [("S", f"P {t}"), (f"Q{t & 1}", q)], [("dV", "dV")])
+            yield ("mma", [("K", k)], [("S", f"dQ {t}")])
+            yield ("commit", "dq_full")
+            yield ("mma", [(f"Q{t & 1}", q)], [("dK", "dK")])
+            yield ("commit", f"dk_done{t & 1}")
+
+    def elementwise():
+        for t in range(n):
+            yield ("wait", "st_full", t)
+            yield ("access", [], [("S", f"P {t}")], 2.0)
+            yield ("arrive", "pt_full")
+
+    def dq():
+        for t in range(n):
+            yield ("wait", "dq_full", t)
+            yield ("access", [("S", f"dQ {t}")], [], 1.0)
+            yield ("arrive", "dq_free")
+            yield ("wait", f"dk_done{t & 1}", t >> 1)
+            yield ("access", [], [(f"Q{t & 1}", f"staged {t}")], 1.0)
+            yield ("arrive", f"q_empty{t & 1}")
+
+    def tail():
+        tails = 0
+        if cut_k:
+            yield ("wait", "t_land", tails)
+            tails += 1
+            yield ("access", [("K", "K")], [], 0.1)
+            yield ("access", [], [("K", "K clean")], 1.0)
+            yield ("arrive", "t_clean")
+        for t in range(per_head - 1 - first % per_head, n, per_head):
+            if not cut_q:
+                break
+            yield ("wait", "t_land", tails)
+            tails += 1
+            yield ("access", [(f"Q{t & 1}", f"Q {t}")], [], 0.1)
+            yield ("access", [], [(f"Q{t & 1}", f"Q {t} clean")], 1.0)
+            yield ("arrive", "t_clean")
+
+    roles = {"producer": producer, "mma": mma, "elementwise": elementwise, "dq": dq, "tail": tail}
+    for name, role in roles.items():
+        sim.run(name, role())
+    return set(roles)
+
+
+def _units(rng, count):
+    return [(rng.choice([0, 1, 1, 2, 3, 5]), rng.random() < 0.5) for _ in range(count)]
+
+
+def _outcome(build, seed):
+    sim = Sim(seed)
+    try:
+        roles = build(sim)
+        sim.go()
+    except Hazard as e:
+        return str(e)
+    return None if sim.finished == roles else f"left waiting: {sorted(roles - sim.finished)}"
+
+
+@pytest.mark.parametrize("count", [1, 4, 12])
+def test_forward_tail_has_no_hazard_and_finishes(count):
+    for seed in range(100):
+        units = _units(random.Random(100 * count + seed), count)
+        assert _outcome(lambda sim: forward_tail(sim, units), seed) is None, (units, seed)
+
+
+@pytest.mark.parametrize("mistake", ["no_wait", "tail_watches_the_ring"])
+def test_the_model_catches_a_wrong_forward_tail(mistake):
+    """Without the wait the PV reads rows of the next sequence. A tail warp that watches the ring by itself, without
+    taking part in it, can be a whole ring away from the MMA thread, where a parity wait means nothing."""
+    caught = sum(_outcome(lambda sim: forward_tail(sim, _units(random.Random(seed), 10), **{mistake: True}), seed) is not None
+                 for seed in range(100))
+    assert caught > 0
+
+
+@pytest.mark.parametrize("heads,per_head", [(1, 1), (1, 4), (2, 3), (4, 1)])
+@pytest.mark.parametrize("cut_k", [False, True])
+@pytest.mark.parametrize("cut_q", [False, True])
+def test_backward_tail_has_no_hazard_and_finishes(heads, per_head, cut_k, cut_q):
+    n = heads * per_head
+    for seed in range(30):
+        lo = random.Random(seed).randrange(n)  # a part of the block's steps
+        for first, last in ((0, n), (lo, n), (0, lo + 1)):
+            assert _outcome(lambda sim: backward_tail(sim, heads, per_head, cut_k, cut_q, first, last), seed) is None
+
+
+def test_the_model_catches_a_backward_tail_without_its_wait():
+    caught = sum(_outcome(lambda sim: backward_tail(sim, 2, 2, True, True, no_wait=True), seed) is not None
+                 for seed in range(60))
+    assert caught > 0
+
+
+def test_the_shares_of_the_paged_decode_cover_every_tile_once():
+    """The arithmetic of csrc/attn_paged.cu: the shares [i W / N, (i + 1) W / N) of the entry list, the first and the
+    last CTA of a pair's tiles as the cuts name them, and at most two parts per CTA."""
+    rng = random.Random(5)
+    for _ in range(300):
+        cost, Hkv, grid = rng.choice([1, 2, 4]), rng.choice([1, 2, 3, 8]), rng.choice([1, 7, 148, 296])
+        tiles = [rng.choice([0, 1, 2, rng.randint(1, 70)]) for _ in range(rng.randint(1, 12))]
+        pairs = [(b, g, t) for b, t in enumerate(tiles) for g in range(Hkv) if t > 0]
+        W = sum(t + cost for _, _, t in pairs)
+        N = min((W + 3) // 4, grid)
+        if N == 0:
+            continue
+        owner = {}
+        parts = [0] * N
+        base = 0
+        for b, g, t in pairs:
+            x0, x1 = base + cost, base + cost + t - 1
+            ctas = []
+            for x in range(x0, x1 + 1):
+                i = ((x + 1) * N - 1) // W
+                assert i * W // N <= x < (i + 1) * W // N  # the CTA whose share holds the entry
+                ctas.append(i)
+                owner[(b, g, x - x0)] = i
+            assert ctas == sorted(ctas) and len(set(ctas)) == ctas[-1] - ctas[0] + 1 or t == 0
+            if ctas[0] != ctas[-1]:
+                for i in set(ctas):
+                    parts[i] += 1
+            base += t + cost
+        assert len(owner) == sum(t for _, _, t in pairs) and max(parts) <= 2
+
+
+def test_the_parts_of_a_plan_fit_their_slots():
+    """make_plan's bounds (csrc/attn_varlen.cu): with blocks cut by rounding their work / max(least, ceil(all work /
+    share)), at most 4 share / 3 parts are joined and at most `share` units come beyond one per block."""
+    rng = random.Random(6)
+    for _ in range(2000):
+        share, least = rng.randint(1, 160), rng.choice([2, 6, 8])
+        work = [rng.choice([0, 1, rng.randint(1, 20), rng.randint(1, 2000)]) for _ in range(rng.randint(1, 40))]
+        size = max(least, -(-sum(work) // share))
+        parts = [max(1, (w + size // 2) // size) for w in work]
+        assert sum(n for n in parts if n > 1) <= 4 * share // 3 + 1
+        assert sum(parts) <= len(work) + share
+        for w, n in zip(work, parts):
+            cuts = [k * w // n for k in range(n + 1)]
+            assert cuts[0] == 0 and cuts[-1] == w and all(a < b for a, b in zip(cuts, cuts[1:])) or n == 1
