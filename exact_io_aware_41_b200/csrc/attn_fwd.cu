@@ -31,6 +31,10 @@
 // waits for the PV that reads P. At d <= 64 the O accumulators are narrow enough to leave TMEM
 // columns for P buffers of its own: the next S of a tile is computed as soon as the softmax has
 // read the current one, overlapping that tile's own softmax.
+//
+// Packed sequences (VL): the units come from a plan in device memory (attn_varlen.cu) instead of the grid's
+// arithmetic, the producer passes their entries on with the claim, and warp 3 zeroes what V tiles hold behind a
+// sequence's end. Everything else is the same code.
 #include <cuda_bf16.h>
 #include <math.h>
 

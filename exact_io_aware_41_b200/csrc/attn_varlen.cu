@@ -4,7 +4,13 @@
 // The lengths are in device memory, so the host can size the launch only by bounds. A plan kernel of one
 // block checks the offsets and lists the blocks of work of every sequence, heaviest first (a counting sort by
 // the number of tiles a block walks), with where each block lies; the prefill kernel's CTAs claim blocks of
-// that list. Launched programmatically, the main kernel sets up while the plan runs.
+// that list. Launched programmatically, the main kernel sets up while the plan runs. Where there are few blocks,
+// long ones are cut into parts along their keys (backward: their steps), whose results are joined by a last kernel.
+//
+// The main kernels are those of the dense entry points (attn_fwd.cu, attn_bwd.cu) with another list of units; what
+// bounds them is said there. Measured beside them on equal shapes (4 sequences of 2048, 16 heads, causal, d = 128,
+// the plan included): forward 87.5 us against 80.5 us, backward 286 us against 264.5 us; 2 of 4096: 150 us against
+// 141 us, 477 us against 446 us.
 #include <cuda_bf16.h>
 #include <math.h>
 

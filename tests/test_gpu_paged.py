@@ -247,6 +247,39 @@ def test_append_leaves_out_and_flags_rows_without_a_place(lib):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_append_on_another_stream_and_captured(lib):
+    """Eager on a side stream, and captured once and replayed with new rows, lengths and pages."""
+    import torch
+
+    lens, new, Hkv, d, page = [70, 5, 33], [7, 5, 1], 2, 64, 16
+    kp, vp, table, kv_lens, _, _ = make_cache(8850, lens, page, Hkv, d, fill=3.0)
+    start, cu = [kp.clone(), vp.clone()], offsets(new)
+    rows = [torch.randn((sum(new), Hkv, d), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    lib.attn_cache_append(*rows, kp, vp, table, kv_lens, cu_seqlens=cu, stream=side)
+    side.synchronize()
+    want = [t.clone() for t in start]
+    _append_plain(*want, *rows, table, lens, new)
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.attn_cache_append(*rows, kp, vp, table, kv_lens, cu_seqlens=cu)
+    for lens, new in (([70, 5, 33], [7, 5, 1]), ([64, 6, 1], [12, 0, 1]), ([13, 4, 40], [9, 4, 0])):
+        for t in rows:
+            t.normal_()
+        kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        cu.copy_(offsets(new))
+        kp.copy_(start[0])
+        vp.copy_(start[1])
+        graph.replay()
+        want = [t.clone() for t in start]
+        _append_plain(*want, *rows, table, lens, new)
+        assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+    assert lib.attn_get_last_error() == lib.ATTN_OK
+    del graph
+
+
 def test_decode_on_another_stream_and_in_graphs_that_share_a_workspace(lib):
     """Two graphs over one workspace, replayed one after the other, and eager calls on a side stream."""
     import torch

@@ -347,6 +347,84 @@ def test_two_streams_at_once(lib):
             assert torch.equal(o, o1) and torch.equal(lse, lse1)
 
 
+def test_backward_on_another_stream_and_in_graphs_that_share_workspaces(lib):
+    """Two graphs (one with few blocks, cut into parts, one with many) over the same workspaces, replayed in turn, and
+    eager calls on a side stream. dQ is a sum of fp32 atomics: equal up to one bf16 step."""
+    import torch
+
+    Hq, Hkv, d = 4, 2, 128
+    sets = []
+    for i, lens in enumerate(([900, 1, 300], [60] * 150)):
+        qb, kb, vb = draw_packed(7980 + i, lens, lens, Hq, Hkv, d)
+        sets.append(([gpu(x) for x in (qb, kb, vb)], gpu(synth.normal_bf16(7980 + i, STREAM_DO, qb.shape)), offsets(lens)))
+
+    def same(got, want):
+        assert torch.allclose(got[0].float(), want[0].float(), rtol=2.0 ** -7, atol=1e-3)
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+    fwd = [lib.attn_fwd_varlen(*x, cu, causal=True) for x, _, cu in sets]
+    want = [lib.attn_bwd_varlen(*x, *f, do, cu, causal=True) for (x, do, cu), f in zip(sets, fwd)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for (x, do, cu), f, w in zip(sets, fwd, want):
+        got = lib.attn_bwd_varlen(*x, *f, do, cu, causal=True, stream=side)
+        side.synchronize()
+        same(got, w)
+    sizes = [(cu.numel() - 1, x[0].shape[0], x[1].shape[0]) for x, _, cu in sets]
+    ws_f = torch.empty(max(lib.attn_fwd_varlen_workspace_bytes(*n, Hq, d) for n in sizes), dtype=torch.uint8,
+                       device="cuda")
+    ws_b = torch.empty(max(lib.attn_bwd_varlen_workspace_bytes(*n, Hq, Hkv, d) for n in sizes), dtype=torch.uint8,
+                       device="cuda")
+    graphs, outs = [], []
+    for x, do, cu in sets:
+        o, lse = torch.empty_like(x[0]), torch.empty((Hq, x[0].shape[0]), device="cuda")
+        g = [torch.empty_like(t) for t in x]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lib.attn_fwd_varlen(*x, cu, causal=True, workspace=ws_f, out=o, lse=lse)
+            lib.attn_bwd_varlen(*x, o, lse, do, cu, causal=True, workspace=ws_b, dq=g[0], dk=g[1], dv=g[2])
+        graphs.append(graph)
+        outs.append((o, lse, g))
+    for i in (0, 1, 0, 0, 1):
+        o, lse, g = outs[i]
+        for t in (o, lse, *g):
+            t.zero_()
+        graphs[i].replay()
+        assert torch.equal(o, fwd[i][0]) and torch.equal(lse, fwd[i][1])
+        same(g, want[i])
+    assert lib.attn_get_last_error() == lib.ATTN_OK
+    del graphs
+
+
+def test_rows_beyond_32_bit_offsets(lib):
+    """The last sequence lies more than 2^31 elements behind the start of q, o, dq: its rows equal the oracle's."""
+    import torch
+
+    Hq, Hkv, d, n = 128, 8, 128, 130
+    lens = [128] * 1024 + [n]  # 131072 rows of 16384 elements before it
+    T = sum(lens)
+    qb, kb, vb = draw_packed(7990, [n], [n], Hq, Hkv, d)
+    dob = synth.normal_bf16(7990, STREAM_DO, qb.shape)
+    q, do = (torch.zeros((T, Hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros((T, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t, x in ((q, qb), (k, kb), (v, vb), (do, dob)):
+        t[T - n:] = gpu(x)
+    cu, sc = offsets(lens), 1 / math.sqrt(d)
+    o, lse = lib.attn_fwd_varlen(q, k, v, cu, scale=sc, causal=True)
+    grads = lib.attn_bwd_varlen(q, k, v, o, lse, do, cu, scale=sc, causal=True)
+    torch.cuda.synchronize()
+    assert lib.attn_get_last_error() == lib.ATTN_OK
+    x = [f64(b) for b in (qb, kb, vb, dob)]
+    O, L, bO, bL = reference(*x[:3], [n], [n], sc, True)
+    assert_within(host(o[T - n:]), O, bO, "O")
+    assert_lse(lse[:, T - n:].cpu().numpy().astype(np.float64), L, bL, "LSE")
+    want, bounds = grad_bounds(*x, O, bO, [n], [n], sc, True)
+    for name, g, w, b in zip(("dQ", "dK", "dV"), grads, want, bounds):
+        assert_within(host(g[T - n:].contiguous()), w, b, name)
+    # zero inputs before it: O and every gradient are zero there
+    assert not bool(o[:T - n].any()) and not any(bool(g[:T - n].any()) for g in grads)
+
+
 def test_single_sequence_agrees_with_the_dense_entry_point(lib):
     """One sequence: the same tiles in the same order as attn_fwd."""
     import torch
