@@ -391,8 +391,10 @@ const char* attn_kernel_name(int which) {
     case 1: return "attn::decode_split_tc_kernel<D,G> (d <= 128), attn::decode_split_kernel<D,G> (d = 256)";
     case 2: return "attn::decode_combine_kernel<D>";
     case 3: return "attn::attn_bwd_pre_kernel, attn::attn_bwd_kernel<VL>, attn::attn_bwd_post_kernel";
-    case 4: return "attn::varlen_plan_kernel, attn::attn_fwd_kernel<D, F8, PAIR, VL>; backward: attn::varlen_bwd_pre_kernel, attn::attn_bwd_kernel<VL>, attn::varlen_bwd_post_kernel";
-    case 5: return "attn::decode_paged_kernel<D, NH>, attn::decode_paged_join_kernel<D, NH>";
+    case 4:
+      return "attn::varlen_plan_kernel, attn::attn_fwd_kernel<D, F8, PAIR, VL>, attn::varlen_join_kernel<D>; "
+             "backward: attn::varlen_bwd_pre_kernel, attn::attn_bwd_kernel<VL>, attn::varlen_bwd_post_kernel";
+    case 5: return "attn::decode_paged_kernel<D, NH>, attn::decode_paged_join_kernel<D, NH, NWARP>";
     case 6: return "attn::cache_append_kernel";
   }
   return nullptr;
