@@ -45,8 +45,8 @@ __device__ __forceinline__ int page_in_pool(int p, int n_pages) {
 // MMA with a token's two heads per lane; movmatrix transposes the bf16 P into the B operand.
 //
 // Bound by HBM: 8 sequences of 1024 to 131072 tokens, 32 heads in groups of 4, d = 128 (1.90 GB): 283-289 us,
-// 6.6-6.7 TB/s, at or a little above a plain copy's rate. Short calls are bound by latency: the scan of the lengths, the page numbers, the first
-// tile and the join follow each other (9 us for 129 tokens).
+// 6.6-6.7 TB/s, at or a little above a plain copy's rate. Short calls are bound by latency: the scan of the lengths,
+// the page numbers, the first tile and the join follow each other (9 us for 129 tokens).
 // ---------------------------------------------------------------------------------------------
 constexpr int kPagedMaxCtas = 320;   // most CTAs of a launch (two per SM; bounds the workspace)
 constexpr int kPagedMinShare = 4;    // entries of a share, at least (fewer CTAs for little work)
@@ -630,7 +630,8 @@ attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStre
 // threads look up where each row goes (the sequence by bisection of the offsets, its length, the page from the
 // table: three dependent reads; -1 for a row that is not written), and then stores them.
 // Bound by memory: every row is read and written once (2 * 2 * Hkv * d bytes per token): 8192 rows of 8 heads of 128
-// (67 MB) in 15.1 us, 4.4 TB/s with the launch, at 6 rows per block; fixed at 1 / 2 / 4 / 8 rows 29.1 / 18.8 / 15.6 / 14.9 us.
+// (67 MB) in 15.1 us, 4.4 TB/s with the launch, at 6 rows per block; fixed at 1 / 2 / 4 / 8 rows
+// 29.1 / 18.8 / 15.6 / 14.9 us.
 constexpr int kAppendRows = 8;    // most rows of one block
 constexpr int kAppendThreads = 256;
 constexpr int kAppendUnits = 4;   // units of K, and of V, that a thread holds

@@ -229,8 +229,29 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // Joins the parts of the query blocks whose keys were cut: a warp per row and head, LSE = log sum_s exp(lse_s),
 // O = sum_s exp(lse_s - LSE) o_s over the parts in order; parts with lse_s = -inf are not read. Bound by memory: fp32
-// parts of 256 rows are read once, mostly from L2.
+// parts of 256 rows are read once, mostly from L2; with few rows by latency, so that the loads of kJoinAhead parts are
+// in flight together (one part after the other, calls with cut blocks took 3-5 % longer: 512 queries over 4096 keys,
+// 8 heads, d = 128 36.3 us against 34.8; 64 over 60000 79.8 against 75.5).
 constexpr int kJoinWarps = 8;
+constexpr int kJoinAhead = 4;  // parts whose loads are in flight together
+
+// N consecutive floats, aligned to min(16, 4 N) bytes.
+template <int N>
+__device__ __forceinline__ void load_row(float (&x)[N], const float* src) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src + e);
+      x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(src);
+    x[0] = v.x, x[1] = v.y;
+  } else {
+    x[0] = *src;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     varlen_join_kernel(const int* count, const VarJoin* joins, const float* part_o, const float* part_lse,
@@ -245,22 +266,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const VarJoin j = joins[w / kFwdBlockRows / Hq];
     if (r >= j.rows) continue;
     auto slot = [&](int s) -> size_t { return (size_t(j.part + s) * Hq + h) * kFwdBlockRows + r; };
-    float mx = -INFINITY;
-    for (int s = lane; s < j.parts; s += 32) mx = fmaxf(mx, part_lse[slot(s)]);
+    const float first_lse = lane < j.parts ? part_lse[slot(lane)] : -INFINITY;
+    float mx = first_lse;
+    for (int s = lane + 32; s < j.parts; s += 32) mx = fmaxf(mx, part_lse[slot(s)]);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
     const float ref = mx == -INFINITY ? 0.f : mx;
     float z = 0.f, acc[EPL];
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-    for (int s = 0; s < j.parts; ++s) {
-      const float l = part_lse[slot(s)];
-      if (l == -INFINITY) continue;
-      const float f = expf(l - ref);
-      z += f;
-      const float* src = part_o + slot(s) * D + lane * EPL;
+    for (int s0 = 0; s0 < j.parts; s0 += 32) {
+      const float mine = s0 == 0 ? first_lse : s0 + lane < j.parts ? part_lse[slot(s0 + lane)] : -INFINITY;
+      const int n = min(32, j.parts - s0);
+      for (int s = 0; s < n; s += kJoinAhead) {
+        float l[kJoinAhead], x[kJoinAhead][EPL];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
+        for (int k = 0; k < kJoinAhead; ++k) {
+          l[k] = __shfl_sync(0xffffffffu, mine, (s + k) & 31);
+          if (s + k >= n) l[k] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) x[k][e] = 0.f;
+          if (l[k] != -INFINITY) load_row<EPL>(x[k], part_o + slot(s0 + s + k) * D + lane * EPL);
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+          const float f = l[k] == -INFINITY ? 0.f : expf(l[k] - ref);
+          z += f;
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) acc[e] = fmaf(f, x[k][e], acc[e]);
+        }
+      }
     }
     const float inv = z != 0.f ? 1.f / z : 0.f;
     __nv_bfloat16* dst = o + (size_t(j.row + r) * Hq + h) * D + lane * EPL;
