@@ -348,12 +348,18 @@ VarPlan plan_at(void* workspace, long long max_units) {
 
 // Forward: into how many shares the tiles are cut for blocks to be cut into parts of a share's size; 0: no block is
 // cut. Keys are cut where there are too few blocks to keep the CTAs busy and enough keys that one could be long: the
-// parts cost up to 39 MB of workspace and a kernel to join them, which many blocks, or short ones, do not pay back.
-int fwd_share(int S, int Tq, int Tk, int Hq, int d) {
-  const int ctas = fwd_varlen_ctas(d);
-  if (Tk < 2 * PlanFwd::kMinPart * kTileRows || fwd_max_blocks(S, Tq) * Hq > 2ll * ctas) return 0;
-  return ctas / Hq;
+// parts cost up to 78 MB of workspace (d = 128) and a kernel to join them, which many blocks, or short ones, do not pay
+// back. two_heads: where no block can have more than 128 queries and units take two heads, there are half as many
+// units (as many shares as without: 64 queries over 60000 keys, 8 heads in a group, 74.9 us against 57.1; 16 sequences
+// of 4 over 40 to 9000 keys, 32 heads 149 us against 109; 18 of 2 over 1600 each, which gain nothing from parts, 69.2
+// against 71.3).
+int fwd_share(int S, int Tq, int Tk, int Hq, int d, bool two_heads) {
+  const long long ctas = fwd_varlen_ctas(d), units_of = two_heads ? 2 : 1;
+  if (Tk < 2 * PlanFwd::kMinPart * kTileRows || fwd_max_blocks(S, Tq) * Hq > 2 * units_of * ctas) return 0;
+  return int(units_of * ctas / Hq);
 }
+// Whether units may take two heads in every block (attn_fwd.cu's var_two_heads; the group has to be even as well).
+bool fwd_two_heads(int Tq, int d) { return Tq <= kTileRows && d <= 128; }
 
 // The forward workspace: its size, and where its parts are (workspace may be null).
 size_t fwd_space(void* workspace, int S, int Tq, int Tk, int Hq, int d, int share, VarPlan* plan) {
@@ -560,7 +566,10 @@ extern "C" {
 size_t attn_fwd_varlen_workspace_bytes(int S, int Tq, int Tk, int Hq, int d) {
   if (S < 1 || Tq < 1 || Tk < 1 || Hq < 1 || d < 1 || S > kVarMaxSeqs) return 0;
   VarPlan plan;
-  return fwd_space(nullptr, S, Tq, Tk, Hq, d, fwd_share(S, Tq, Tk, Hq, d), &plan);
+  const size_t one = fwd_space(nullptr, S, Tq, Tk, Hq, d, fwd_share(S, Tq, Tk, Hq, d, false), &plan);
+  if (!fwd_two_heads(Tq, d)) return one;
+  const size_t two = fwd_space(nullptr, S, Tq, Tk, Hq, d, fwd_share(S, Tq, Tk, Hq, d, true), &plan);
+  return two > one ? two : one;
 }
 
 attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const int32_t* cu_q, const int32_t* cu_k,
@@ -571,7 +580,7 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, const
   attn_status_t st =
       varlen_args_status(ptrs, 4, lse, cu_q, cu_k, S, Tq, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, scale, causal);
   if (st != ATTN_OK) return st;
-  const int share = fwd_share(S, Tq, Tk, Hq, d);
+  const int share = fwd_share(S, Tq, Tk, Hq, d, fwd_two_heads(Tq, d) && Hq / Hkv % 2 == 0);
   VarPlan plan;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < fwd_space(workspace, S, Tq, Tk, Hq, d, share, &plan))

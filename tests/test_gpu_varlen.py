@@ -92,6 +92,22 @@ def test_forward_keys_cut_into_parts(lib, d, causal, case):
     _check_forward(lib, 7350 + 10 * case + d + int(causal), ql, kl, Hq, Hkv, d, causal)
 
 
+FEW_QUERIES = [
+    ([64], [6000], 8, 1),                       # one block, units of two heads: their keys in many parts
+    ([1, 0, 126, 1], [2500, 40, 1999, 3], 6, 3),
+    ([128], [3000], 4, 4),                      # no second head in the group
+    ([3] * 40, [50] * 39 + [2000], 16, 2),      # more blocks than CTAs, fewer units than twice that
+]
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("case", range(len(FEW_QUERIES)))
+def test_forward_few_queries_over_many_keys(lib, d, causal, case):
+    ql, kl, Hq, Hkv = FEW_QUERIES[case]
+    _check_forward(lib, 7150 + 10 * case + d + int(causal), ql, kl, Hq, Hkv, d, causal)
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_parts_do_not_take_rows_of_others(lib, d):
     """Blocks cut into parts beside sequences of NaN, and rows that see keys of the last part only (more queries
