@@ -373,19 +373,19 @@ __global__ void __launch_bounds__(bwd::THREADS, 1)
     if (VL && warp == 3) {
       // ================================ tail rows ================================
       // dV, dK sum over the queries of a tile and dQ over its keys: P = dS = 0 does not cancel NaN or infinities in
-      // rows of the next sequence, so those are zeroed once the tile has landed, while the elementwise warps work. The phases of t_land may lie many steps apart,
-      // whose own waits are bounded and end this one, hence its own limit.
+      // rows of the next sequence, so those are zeroed once the tile has landed, while the elementwise warps work.
+      // The phases of t_land may lie many steps apart, whose own waits are bounded and end this one, hence its own
+      // limit.
       constexpr uint64_t kTailLimit = 512 * kWaitLimitNs;
       int tails = 0;
       // zeroes rows [cut, 128) of n tiles at `tile`, once the next phase of t_land is there
       auto clean = [&](uint8_t* tile, int n, int cut) -> bool {
         if (!__all_sync(0xffffffffu, mbar_wait(t_land, uint32_t(tails++ & 1), abort_flag, kTailLimit))) return false;
-        const int rows = 128 - cut;
-        for (int i = lane; i < n * rows * 16; i += 32) {
-          const int r = cut + (i / 16) % rows, u = i % 16, which = i / 16 / rows;  // whole rows: swizzled or not
-          *reinterpret_cast<uint4*>(tile + which * TILE_BYTES + (u / 8) * CHUNK_BYTES + r * 128 + (u % 8) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
+        const int u = lane & 15;  // of a row's 16-byte units; whole rows are zeroed, so the swizzle does not matter
+        uint8_t* unit = tile + (u / 8) * CHUNK_BYTES + (u % 8) * 16;
+        for (int which = 0; which < n; ++which, unit += TILE_BYTES)
+#pragma unroll 4
+          for (int r = cut + (lane >> 4); r < 128; r += 2) *reinterpret_cast<uint4*>(unit + r * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(t_clean);

@@ -271,8 +271,8 @@ __device__ __forceinline__ Unit unit_var(const FwdArgs& a, int h, const VarEntry
   u.n_tiles = min(u.n_tiles, entry.cut.x);
   u.n_tile0 = min(u.n_tile0, u.n_tiles);
   // One tile of queries and no second head: the second tile takes them and the first one takes no part, as one whose
-  // rows see no key. (64 prompts of 100 tokens, 32 heads, d = 128: 80 us with an empty
-  // tile, 68 us without, 51 us with two heads.)
+  // rows see no key. (64 prompts of 100 tokens, 32 heads, d = 128: 80 us with an empty tile, 68 us without, 51 us
+  // with two heads.)
   u.two_heads = var_two_heads<D, PAIR>(a, u.nq);
   u.skip = C::NQT == 2 && u.nq <= C::BM && !u.two_heads ? C::BM : 0;
   if (u.skip) u.n_tile0 = 0;
@@ -907,7 +907,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, PAIR>::THREADS, 1)
       const int nq = VL ? un.nq : args.Nq, nkv = VL ? un.nkv : args.Nkv;
       const int diag = nkv - nq;  // key j visible to query i iff j <= i + diag
       const int head = un.h + (VL && un.two_heads ? qt : 0);
-      const int q_first = (VL ? -un.skip : un.q0) + (VL && un.two_heads ? 0 : qt + int(rank)) * C::BM;  // (a pair: NQT = 1, rank 1 takes the second 128 rows)
+      // (a pair: NQT = 1, rank 1 takes the second 128 rows)
+      const int q_first = (VL ? -un.skip : un.q0) + (VL && un.two_heads ? 0 : qt + int(rank)) * C::BM;
       const int q_row = q_first + row;
       // last key visible to this row (any key index <= lim is visible); rows past nq are padding
       const int lim = args.causal ? min(nkv - 1, q_row + diag) : nkv - 1;

@@ -414,10 +414,12 @@ struct BwdSpace {
   long long acc_rows, lse_rows;
 };
 
-// Block 0 makes the plan. The others take a packed query row per warp, 16 lanes per head: D = sum_e dO_e O_e and
-// LSE' = LSE log2 e (+inf for a row without keys, so that its P is 0), and the row of the accumulator zeroed, with
-// the padding rows of its last box after a sequence's last row. Every place a row of a sequence writes to lies
-// inside the arrays whatever the other offsets are; offsets out of order leave results unused (the plan says so).
+// Block 0 makes the plan. The others zero the accumulator, all of it, in equal shares (left to the warps of the rows,
+// with the rest of a sequence's last box, one SM zeroes nearly all of it where sequences are short: 100 of one token,
+// 16 heads, the whole backward 368 us against 109), and take a packed query row per
+// warp, 16 lanes per head: D = sum_e dO_e O_e and LSE' = LSE log2 e (+inf for a row without keys, so that its P is 0).
+// Every place a row of a sequence writes to lies inside the arrays whatever the other offsets are; offsets out of
+// order leave results unused (the plan says so).
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                           const float* __restrict__ lse, const int32_t* __restrict__ cu_q,
@@ -429,6 +431,13 @@ __global__ void __launch_bounds__(kPlanThreads)
     return;
   }
   const int lane = threadIdx.x & 31, seg = lane & 15;
+  {
+    float4* acc = reinterpret_cast<float4*>(w.acc);
+    const size_t n = size_t(w.acc_rows) * Hq * (bwd::D / 4), step = size_t(gridDim.x - 1) * kPlanThreads;
+#pragma unroll 4
+    for (size_t i = size_t(blockIdx.x - 1) * kPlanThreads + threadIdx.x; i < n; i += step)
+      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   const int n_warps = int(gridDim.x - 1) * (kPlanThreads / 32);
   for (long long t = (blockIdx.x - 1ll) * (kPlanThreads / 32) + (threadIdx.x >> 5); t < Tq; t += n_warps) {
     int s = seq_of_row(cu_q, S, int(t));
@@ -439,7 +448,6 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (lane == 0) w.row_of[t] = s < 0 ? -1 : int(acc_row);
     if (s < 0) continue;
     const size_t lse_row = padded_row(first, s, kTileRows) + i;
-    const int zero_rows = i + 1 == cu_q[s + 1] - first ? (i / kAccRows + 1) * kAccRows - i : 1;
     for (int h0 = 0; h0 < Hq; h0 += 2) {
       const int h = h0 + (lane >> 4);
       const bool real = h < Hq;
@@ -453,11 +461,6 @@ __global__ void __launch_bounds__(kPlanThreads)
         for (int k = 0; k < 4; ++k) {
           dsum = fmaf(__uint_as_float(wa[k] << 16), __uint_as_float(wc[k] << 16), dsum);
           dsum = fmaf(__uint_as_float(wa[k] & 0xFFFF0000u), __uint_as_float(wc[k] & 0xFFFF0000u), dsum);
-        }
-        for (int r = 0; r < zero_rows; ++r) {
-          float4* z = reinterpret_cast<float4*>(w.acc + ((acc_row + r) * Hq + h) * bwd::D) + 2 * seg;
-          z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-          z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
 #pragma unroll
@@ -640,8 +643,10 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
     return ATTN_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  // a warp per row, at most two blocks of them per SM
-  const long long want = ((long long)Tq + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
+  // a warp per row and at most 4 stores of zeros per thread, on at most two blocks per SM
+  const long long by_row = ((long long)Tq + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
+  const long long by_zero = (w.acc_rows * Hq * (bwd::D / 4) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  const long long want = by_row > by_zero ? by_row : by_zero;
   const unsigned rows_grid = unsigned(want < 2ll * sms ? want : 2ll * sms);
   varlen_bwd_pre_kernel<<<1 + rows_grid, kPlanThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), lse, cu_q, cu_k, S, Tq, Tk, Hq,

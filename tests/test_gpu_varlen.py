@@ -92,6 +92,19 @@ def test_forward_keys_cut_into_parts(lib, d, causal, case):
     _check_forward(lib, 7350 + 10 * case + d + int(causal), ql, kl, Hq, Hkv, d, causal)
 
 
+PLANNED = [
+    [5] * 40 + [2600] + [1] * 3,                # 8 threads of the plan to a sequence, one of 11 blocks
+    [8300, 3],                                  # a warp to a sequence, one of 33 blocks
+    [1] * 127 + [300],
+    [2] * 129 + [2400],                         # a thread to a sequence, a warp to the long one
+]
+
+
+@pytest.mark.parametrize("case", range(len(PLANNED)))
+def test_forward_plans_of_every_kind(lib, case):
+    _check_forward(lib, 7140 + case, PLANNED[case], PLANNED[case], 1, 1, 64, True)
+
+
 FEW_QUERIES = [
     ([64], [6000], 8, 1),                       # one block, units of two heads: their keys in many parts
     ([1, 0, 126, 1], [2500, 40, 1999, 3], 6, 3),
@@ -165,6 +178,7 @@ BACKWARD = [
     ([1500], [1400], 8, 1),                     # few key blocks with many steps: each cut into parts
     ([2500, 3], [130, 40], 2, 2),
     ([40] * 300, [40] * 300, 2, 2),             # many blocks, none of them cut
+    ([30] * 40, [20] * 39 + [1500], 1, 1),      # 8 threads of the plan to a sequence, one of 12 blocks
 ]
 
 
