@@ -416,11 +416,14 @@ struct BwdSpace {
 
 // Block 0 makes the plan. The others zero the accumulator, all of it, in equal shares (left to the warps of the rows,
 // with the rest of a sequence's last box, one SM zeroes nearly all of it where sequences are short: 100 of one token,
-// 16 heads, the whole backward 368 us against 109), and take a packed query row per
-// warp, 16 lanes per head: D = sum_e dO_e O_e and LSE' = LSE log2 e (+inf for a row without keys, so that its P is 0).
-// Every place a row of a sequence writes to lies inside the arrays whatever the other offsets are; offsets out of
-// order leave results unused (the plan says so).
-__global__ void __launch_bounds__(kPlanThreads)
+// 16 heads, the whole backward 368 us against 109), and take a packed query row per warp, 16 lanes per head:
+// D = sum_e dO_e O_e and LSE' = LSE log2 e (+inf for a row without keys, so that its P is 0). Every place a row of a
+// sequence writes to lies inside the arrays whatever the other offsets are; offsets out of order leave results unused
+// (the plan says so). Bound by memory: with the plan's 54 registers one block fits on an SM and too few loads are in
+// flight, so two blocks are asked for, at 32 registers with spills in the plan (the backward and forward of 8192 packed
+// tokens 340.5 us against 334.4, the backward of 100 sequences of 100 169 against 160, of 100 single tokens 83.6
+// against 85.0).
+__global__ void __launch_bounds__(kPlanThreads, 2)
     varlen_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                           const float* __restrict__ lse, const int32_t* __restrict__ cu_q,
                           const int32_t* __restrict__ cu_k, int S, int Tq, int Tk, int Hq, int Hkv, int causal, int share,
