@@ -630,11 +630,10 @@ attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStre
 // threads look up where each row goes (the sequence by bisection of the offsets, its length, the page from the
 // table: three dependent reads; -1 for a row that is not written), and then stores them.
 // Bound by memory: every row is read and written once (2 * 2 * Hkv * d bytes per token): 8192 rows of 8 heads of 128
-// (67 MB) in 15.1 us, 4.4 TB/s with the launch, at 6 rows per block; fixed at 1 / 2 / 4 / 8 rows
-// 29.1 / 18.8 / 15.6 / 14.9 us.
-constexpr int kAppendRows = 8;    // most rows of one block
+// (67 MB) in 14.6 us, 4.6 TB/s with the launch, at 8 rows per block; at 1 / 2 / 4 rows
+// 29.1 / 18.8 / 15.6 us.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendUnits = 4;   // units of K, and of V, that a thread holds
+constexpr int kAppendUnits = 4;  // units of K, and of V, that a thread holds
 
 // Place (in 16-byte units of the pools) of packed row t, or -1.
 __device__ __forceinline__ long long append_place(int t, const int32_t* __restrict__ cu,
@@ -676,7 +675,7 @@ __global__ void __launch_bounds__(kAppendThreads)
                         const int32_t* __restrict__ kv_lens, uint4* __restrict__ k_pages, uint4* __restrict__ v_pages,
                         int B, int T, int n_pages, int page_size, int max_pages, int units, long long ks_units,
                         long long vs_units, int rows) {
-  __shared__ long long dst[kAppendRows];  // place of each row in the pools
+  __shared__ long long dst[kAppendThreads];  // place of each row in the pools
   const int t0 = blockIdx.x * rows, total = min(rows, T - t0) * units;
   uint4 k[kAppendUnits], v[kAppendUnits];
   bool placed = false;
@@ -786,12 +785,17 @@ attn_status_t attn_cache_append(const void* k_new, const void* v_new, const int3
   if (cu == nullptr && T != B) return ATTN_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  // one row per block while that leaves SMs idle (latency), up to kAppendRows where there are many
-  const long long per = T / (8ll * sms);
-  const int rows = per < 1 ? 1 : per > kAppendRows ? kAppendRows : int(per);
+  // About three blocks per SM, which run at once; where there are many rows, at most as many per block as keep every
+  // thread's units in flight, and at least 8, for one look-up of their places. (At most 8 rows of any width and up to
+  // eight blocks per SM instead: 63929 rows of 256 bytes 30.7 us against 14.8, 71157 of 64 28.8 against 5.1, 1389 of
+  // 1024 8.0 against 4.3, 8192 of 2048 15.1 against 14.6; with four blocks 12425 rows of 256 take 5.9 us against 4.5.)
+  const int units = Hkv * d / 8, held = kAppendUnits * kAppendThreads / units;
+  const int most = held < 8 ? 8 : held > kAppendThreads ? kAppendThreads : held;
+  const long long per = T / (3ll * sms);
+  const int rows = per < 1 ? 1 : per > most ? most : int(per);
   cache_append_kernel<<<unsigned((T + (long long)rows - 1) / rows), kAppendThreads, 0, stream>>>(
       static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), cu, page_table, kv_lens,
-      static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages), B, T, n_pages, page_size, max_pages, Hkv * d / 8,
+      static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages), B, T, n_pages, page_size, max_pages, units,
       k_stride / 8, v_stride / 8, rows);
   return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : (cudaGetLastError(), ATTN_ERR_CUDA);
 }

@@ -211,6 +211,32 @@ def test_append(lib, page, Hkv, d):
     assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
 
 
+@pytest.mark.parametrize("n,Hkv,d", [(120000, 1, 32), (5000, 1, 64), (30000, 1, 128), (9000, 3, 40), (700, 16, 256)])
+def test_append_many_rows_of_every_width(lib, n, Hkv, d):
+    """Blocks of one row up to as many as they have threads; the last sequences and rows end inside a block."""
+    import torch
+
+    page, lens = 16, [n - 1500 if n > 3000 else n - 400, 1, 0, 377]
+    table = torch.randperm(-(-n // page) + 8, device="cuda").to(torch.int32)
+    need = [-(-x // page) for x in lens]
+    rows = torch.full((4, max(need)), -1, dtype=torch.int32, device="cuda")
+    for b, m in enumerate(need):
+        rows[b, :m] = table[sum(need[:b]):sum(need[:b]) + m]
+    kv_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pools = [torch.full((table.numel(), page, Hkv, d), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = [p.clone() for p in pools]
+    new = [torch.randn((sum(lens) + 5, Hkv, d), device="cuda").to(torch.bfloat16) for _ in range(2)]  # 5 of nobody
+    lib.attn_cache_append(*new, *pools, rows, kv_lens, cu_seqlens=offsets(lens))
+    at = 0
+    for b, m in enumerate(lens):
+        t = torch.arange(m, device="cuda")
+        for w, x in zip(want, new):
+            w[rows[b, t // page].long(), t % page] = x[at:at + m]
+        at += m
+    assert lib.attn_get_last_error() == lib.ATTN_OK
+    assert torch.equal(pools[0], want[0]) and torch.equal(pools[1], want[1])
+
+
 def test_append_one_row_per_sequence_from_a_fused_projection(lib):
     import torch
 
