@@ -75,9 +75,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 
 // A 4-d tiled TMA map: dims[0] innermost (contiguous), dims[i] elements of elem_bytes each, dense
 // strides (row_stride, if not 0, between the indices of dims[2]); box[] elements per dimension; swizzle
-// 128, 64 or 0 bytes.
+// 128, 64 or 0 bytes; reads widened to l2_bytes (64, 128 or 256) in L2.
 static bool encode_map_uncached(CUtensorMap* map, const void* base, int elem_bytes, const long long* dims,
-                                const int* box, unsigned swizzle_bytes, long long row_stride) {
+                                const int* box, unsigned swizzle_bytes, long long row_stride, int l2_bytes) {
   auto fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t gd[4] = {cuuint64_t(dims[0]), cuuint64_t(dims[1]), cuuint64_t(dims[2]), cuuint64_t(dims[3])};
@@ -91,8 +91,11 @@ static bool encode_map_uncached(CUtensorMap* map, const void* base, int elem_byt
   const CUtensorMapDataType dt = elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : elem_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapL2promotion wide = l2_bytes == 64    ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                      : l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                        : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   const CUresult r = fn(map, dt, 4, const_cast<void*>(base), gd, gs, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        wide, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -106,8 +109,11 @@ struct MapKey {
   int box[4];
   unsigned swizzle;
   long long row_stride;
+  int l2_bytes;
   bool operator==(const MapKey& o) const {
-    if (base != o.base || elem_bytes != o.elem_bytes || swizzle != o.swizzle || row_stride != o.row_stride) return false;
+    if (base != o.base || elem_bytes != o.elem_bytes || swizzle != o.swizzle || row_stride != o.row_stride ||
+        l2_bytes != o.l2_bytes)
+      return false;
     for (int i = 0; i < 4; ++i)
       if (dims[i] != o.dims[i] || box[i] != o.box[i]) return false;
     return true;
@@ -128,9 +134,9 @@ MapCache& map_cache() {
 }  // namespace
 
 bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long long* dims, const int* box,
-                unsigned swizzle_bytes, long long row_stride) {
+                unsigned swizzle_bytes, long long row_stride, int l2_bytes) {
   MapKey k{base, elem_bytes, {dims[0], dims[1], dims[2], dims[3]}, {box[0], box[1], box[2], box[3]}, swizzle_bytes,
-           row_stride};
+           row_stride, l2_bytes};
   MapCache& c = map_cache();
   std::lock_guard<std::mutex> lock(c.mu);
   for (int i = 0; i < kMapCacheSize; ++i) {
@@ -139,7 +145,7 @@ bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long l
       return true;
     }
   }
-  if (!encode_map_uncached(map, base, elem_bytes, dims, box, swizzle_bytes, row_stride)) return false;
+  if (!encode_map_uncached(map, base, elem_bytes, dims, box, swizzle_bytes, row_stride, l2_bytes)) return false;
   const int slot = c.next;
   c.next = (c.next + 1) % kMapCacheSize;
   c.key[slot] = k;

@@ -88,9 +88,10 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int d, int heads, int r
 
 // The general form: a 4-d tensor of elem_bytes-sized elements (1: 8-bit codes, 2: bf16, 4: fp32) with dense
 // strides, dims[0] innermost, box[] elements per dimension; cached like encode_tile_map.
-// row_stride, if not 0: elements between consecutive indices of dims[2] (a token stride).
+// row_stride, if not 0: elements between consecutive indices of dims[2] (a token stride). l2_bytes: 64, 128 or 256, the
+// aligned pieces in which L2 fetches what is read.
 bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, const long long* dims, const int* box,
-                unsigned swizzle_bytes, long long row_stride = 0);
+                unsigned swizzle_bytes, long long row_stride = 0, int l2_bytes = 256);
 
 // Opts `func` into `bytes` of dynamic shared memory on the current device. The attribute belongs to
 // the function on one device, so it is set once per (function, device) and again only when a

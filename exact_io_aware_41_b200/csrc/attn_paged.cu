@@ -48,7 +48,14 @@ __device__ __forceinline__ int page_in_pool(int p, int n_pages) {
 // 6.6-6.7 TB/s, at or a little above a plain copy's rate. Short calls are bound by latency: the scan of the lengths,
 // the page numbers, the first tile and the join follow each other (9 us for 129 tokens).
 // ---------------------------------------------------------------------------------------------
-constexpr int kPagedMaxCtas = 320;   // most CTAs of a launch (two per SM; bounds the workspace)
+// CTAs per SM (as many as registers allow: a small head's tile is 8 or 16 KB, and what a CTA does for it, one step
+// after the other, does not shrink with it; 8 x 80000 tokens of 8 heads of 32 200 us with two, 123 with four; 115
+// ragged sequences of 8 heads of 64 in pages of 16 tokens 155 us with two, 137 with three; a ring of twice the depth
+// instead changes nothing), and the most of a launch (which bound the workspace).
+constexpr int paged_ctas_per_sm(int d, int nh) {
+  return d == 256 ? 1 : d == 128 ? 2 : d == 64 ? (nh == 1 ? 3 : 2) : (nh == 1 ? 4 : 3);
+}
+constexpr int paged_max_ctas(int d, int nh) { return 160 * paged_ctas_per_sm(d, nh); }
 constexpr int kPagedMinShare = 4;    // entries of a share, at least (fewer CTAs for little work)
 
 template <int D, int NH>
@@ -68,8 +75,8 @@ struct PagedCfg {
   static constexpr int QUARTER = D / 4 / NW;    // accumulator registers per head block, of D / 4
   static constexpr int MERGE_FLOATS = NW * 2 * HEADS + NW * (NW - 1) * NH * QUARTER * 32;
   static constexpr int MERGE_BYTES = MERGE_FLOATS * 4;
-  static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
-  static constexpr int SMEM_CAP = (CTAS == 1 ? 227 : 113) * 1024;
+  static constexpr int CTAS = paged_ctas_per_sm(D, NH);
+  static constexpr int SMEM_CAP = 227 / CTAS * 1024;  // (228 KB per SM, 1 KB of them reserved per CTA)
   static constexpr int FIT = (SMEM_CAP - 1024 - MERGE_BYTES - 512) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static_assert(STAGES >= 2, "a ring of two stages at least");
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(32 * NWARP)
 }
 
 // Workspace: the cuts, then the part slots.
-constexpr size_t kPagedCutBytes = kPagedMaxCtas * sizeof(int4);
+size_t paged_cut_bytes(int d, int nh) { return paged_max_ctas(d, nh) * sizeof(int4); }
 
 template <int D, int NH>
 attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStream_t stream) {
@@ -599,11 +606,15 @@ attn_status_t launch_paged(PagedArgs a, const void* kp, const void* vp, cudaStre
   const int box[4] = {C::CE, 1, a.box, 1};
   const unsigned swz = D >= 64 ? 128u : 0u;
   CUtensorMap tmK, tmV;
-  if (!encode_map(&tmK, kp, 2, dims, box, swz) || !encode_map(&tmV, vp, 2, dims, box, swz)) return ATTN_ERR_CUDA;
+  // L2 fetches a head's row and not more of its token's: the next head's is read too late to still be there (8 x 40000
+  // tokens of 8 heads of 64: 972 MB from DRAM instead of 655 and 164 us against 126; 8 x 80000 of 4 157 against 107)
+  const int l2 = a.Hkv == 1 || D >= 128 ? 256 : 2 * D;
+  if (!encode_map(&tmK, kp, 2, dims, box, swz, 0, l2) || !encode_map(&tmV, vp, 2, dims, box, swz, 0, l2))
+    return ATTN_ERR_CUDA;
   if (ensure_dyn_smem(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES) != cudaSuccess) return ATTN_ERR_CUDA;
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
-  const int grid = C::CTAS * sms < kPagedMaxCtas ? C::CTAS * sms : kPagedMaxCtas;
+  const int most = paged_max_ctas(D, NH), grid = C::CTAS * sms < most ? C::CTAS * sms : most;
   kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tmK, tmV, a);
   if (cudaPeekAtLastError() != cudaSuccess) return cudaGetLastError(), ATTN_ERR_CUDA;
   cudaLaunchConfig_t lc = {};
@@ -719,8 +730,8 @@ extern "C" {
 
 size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return 0;
-  const size_t heads = Hq / Hkv <= 8 ? 8 : 16;
-  return kPagedCutBytes + 2 * size_t(kPagedMaxCtas) * heads * (size_t(d) + 2) * sizeof(float);
+  const int nh = Hq / Hkv <= 8 ? 1 : 2;
+  return paged_cut_bytes(d, nh) + 2 * size_t(paged_max_ctas(d, nh)) * 8 * nh * (size_t(d) + 2) * sizeof(float);
 }
 
 attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -759,7 +770,7 @@ attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* 
   a.q_stride = q_stride;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.cuts = static_cast<int4*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kPagedCutBytes);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + paged_cut_bytes(d, a.G > 8 ? 2 : 1));
   a.timeout_ns = kWaitLimitNs;
   const bool wide = a.G > 8;
   switch (d) {
