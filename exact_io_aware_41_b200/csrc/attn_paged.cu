@@ -31,11 +31,11 @@ __device__ __forceinline__ int page_in_pool(int p, int n_pages) {
 // Split kernel. The work of a call is the list of 64-token tiles of every (sequence b, kv head g), in that
 // order, with PAIR_COST empty entries before each pair's tiles for what a pair costs by itself (its queries'
 // loads, joining the warps, the output; a batch of 64 between 1 and 4096 tokens, d = 128: 88.6 us without them,
-// 85.4 with one, 86.6 with two; d = 256 with two instead of one: 8 % faster to 6 % slower over eight batches). CTA i of N takes the contiguous share [i W / N, (i + 1) W / N) of the W entries. Every CTA so has the
-// same work whatever the lengths are, and neither the grid nor the workspace depends on the capacity of the page
-// table. A share covers whole (b, g) pairs, whose output is written here, and at its ends parts of pairs that other
-// CTAs share: those leave (m, l, unnormalised O) in a workspace slot, at most two per CTA, and the join kernel
-// below merges them.
+// 85.4 with one, 86.6 with two; d = 256 with two instead of one: 8 % faster to 6 % slower over eight batches). CTA i
+// of N takes the contiguous share [i W / N, (i + 1) W / N) of the W entries. Every CTA so has the same work whatever
+// the lengths are, and neither the grid nor the workspace depends on the capacity of the page table. A share covers
+// whole (b, g) pairs, whose output is written here, and at its ends parts of pairs that other CTAs share: those leave
+// (m, l, unnormalised O) in a workspace slot, at most two per CTA, and the join kernel below merges them.
 //
 // A producer warp streams the tiles through a ring of shared-memory stages with TMA, one box per page (or per
 // 64 tokens of a larger page), one lane per box. Each of the NW consumer warps takes 16 tokens of every tile
